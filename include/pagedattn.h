@@ -50,8 +50,11 @@
  *
  * Supported: head_dim 128; num_qo_heads / num_kv_heads in {1, 2, 4, 8};
  * page_size a power of two in [1, 1024]; fp16 and bf16 q (and pools), and for
- * decode also 8-bit FP8 pools (E4M3 / E5M2 with a K and a V scale) and rotary
- * positions applied on the fly (pa_problem.kv_dtype, rope_theta).
+ * decode also 8-bit FP8 pools (E4M3 / E5M2 with a K and a V scale, or with a
+ * scale for each block of tokens and kv head) and rotary positions applied on
+ * the fly (pa_problem.kv_dtype, rope_theta).  8-bit pools with block scales
+ * are written by pa_kv_append and read back by pa_kv_read; scores may be
+ * capped and biased by distance (pa_attention_options).
  */
 #ifndef PAGEDATTN_H_
 #define PAGEDATTN_H_
@@ -298,6 +301,102 @@ pa_status pa_cascade_run(pa_plan_t plan, const void* q, const void* k_pool,
 pa_status pa_prefill_run(pa_plan_t plan, const void* q, const void* k_pool, const void* v_pool,
                          const int32_t* d_kv_indices, void* o, float* lse, void* d_workspace,
                          size_t workspace_bytes, void* stream);
+/* Further options of a decode or prefill run.  A zeroed struct asks for
+ * nothing: pa_run_options / pa_prefill_run_options then equal pa_run /
+ * pa_prefill_run.
+ *
+ * Block scales (decode, 8-bit pools): k_scales / v_scales hold one fp32 scale
+ * for each block of scale_block tokens and kv head, device arrays
+ * [num_pages * page_size / scale_block, num_kv_heads]; scale_block is a power
+ * of two dividing page_size.  The cached value of pool row r (page * P + row)
+ * is scales[r / scale_block, h] * code, so a block's scale belongs to its
+ * pool rows whatever request they serve.  They take the place of
+ * pa_problem.k_scale / v_scale, which must be 1.  Scales are 0 or of
+ * magnitude 2^-60 to 2^60 (what pa_kv_append writes).
+ *
+ * Scores: with s = sm_scale <q, k> (and the positions' rotation, if any),
+ *   s <- logit_cap * tanh(s / logit_cap)     if logit_cap > 0, then
+ *   s <- s - alibi_slopes[hq] * distance     if alibi_slopes (device, fp32 [Hq]),
+ * where distance is the query token's position minus the key's: L_b - 1 - t
+ * in decode, L_b - Q_b + i - t for new token i of a causal prefill (>= 0 for
+ * every key it sees).  Plans without the causal mask refuse slopes, and
+ * logit_cap must be 0 or in [2^-20, 2^20].  lse is of the final scores. */
+typedef struct {
+  const float* k_scales;
+  const float* v_scales;
+  int32_t scale_block;       /* 0: per-tensor scales (both pointers null) */
+  float logit_cap;           /* 0: no cap */
+  const float* alibi_slopes; /* null: no bias */
+} pa_attention_options;
+
+/* pa_run with options (null options: pa_run).  Cascade, prefill and cache
+ * plans are refused as by pa_run. */
+pa_status pa_run_options(pa_plan_t plan, const pa_attention_options* options, const void* q,
+                         const void* k_pool, const void* v_pool, const int32_t* d_kv_indices,
+                         void* o, float* lse, void* d_workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* pa_prefill_run with options.  Prefill reads 16-bit pools, so block scales
+ * are refused (PA_ERR_UNSUPPORTED): unpack an 8-bit cache with pa_kv_read. */
+pa_status pa_prefill_run_options(pa_plan_t plan, const pa_attention_options* options,
+                                 const void* q, const void* k_pool, const void* v_pool,
+                                 const int32_t* d_kv_indices, void* o, float* lse,
+                                 void* d_workspace, size_t workspace_bytes, void* stream);
+
+/* Cache plan: the last Q_b = qo_indptr[b + 1] - qo_indptr[b] tokens of each
+ * request b, whose pages (kv_indptr / last_page_len as for pa_plan_create)
+ * hold L_b >= Q_b tokens, for pa_kv_append (write them) and pa_kv_read (read
+ * them back).  Their 16-bit rows are rows qo_indptr[b] .. qo_indptr[b + 1] - 1
+ * of k and v, token L_b - Q_b first.  Host only, no CUDA call.  Of the problem
+ * batch, num_kv_heads, head_dim, page_size, dtype (of the rows), kv_dtype
+ * (PA_E4M3 or PA_E5M2), num_pages and PA_FLAG_CHECK_INDICES are used; k_scale
+ * and v_scale must be 1, the rest only has to be valid.  scale_block: tokens
+ * per scale, a power of two dividing page_size.
+ * PA_ERR_INVALID_ARG for malformed tables, Q_b > L_b, a 16-bit kv_dtype or a
+ * scale_block that does not divide the page. */
+pa_status pa_kv_plan_create(const pa_problem* problem, int32_t scale_block,
+                            const int32_t* qo_indptr_host, const int32_t* kv_indptr_host,
+                            const int32_t* last_page_len_host, pa_plan_t* out);
+
+/* Quantise the plan's tokens into the pools as they are written.  k, v:
+ * [total_q, num_kv_heads, 128] rows in `dtype`, consecutive rows k_stride /
+ * v_stride elements apart (>= num_kv_heads * 128, a multiple of 8, so that
+ * rows may be slices of a wider projection).  For each block of scale_block
+ * tokens, kv head, and K and V on its own, with N the block's tokens that are
+ * written and O the tokens that the request already holds in it:
+ *   need  = the smallest power of two in [2^-60, 2^60] with
+ *           max |x| <= MAX * need over the finite elements of N
+ *           (MAX = 448 E4M3, 57344 E5M2);
+ *   scale = need if O is empty (whatever the array held before), else
+ *           max(scale, need);
+ *   codes of O are rounded again to code * (old scale / scale) where the scale
+ *           grew (old scales are finite and > 0; between powers of two this
+ *           is exact but for codes that become subnormal);
+ *   codes of N = x / scale, rounded to nearest even, saturating (infinities
+ *           too); NaN stays NaN.
+ * Nothing else of the pools and scales is written, rows of the block past the
+ * request's last token included.  A block that receives tokens may belong to
+ * one request only (two requests appending into one block race), and no other
+ * work may read or write it meanwhile.  One launch, no synchronisation. */
+pa_status pa_kv_append(pa_plan_t plan, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, void* k_pool, void* v_pool, float* k_scales,
+                       float* v_scales, const int32_t* d_kv_indices, void* d_workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Read the plan's tokens back: scale * code, rounded once to `dtype`.  With
+ * d_out_indices null, into rows of k and v as pa_kv_append takes them.  Else
+ * into pages: k and v are [num_out_pages, page_size, num_kv_heads, 128] pools
+ * and page j of request b goes to page d_out_indices[kv_indptr[b] + j] (the
+ * strides are then num_kv_heads * 128): a prefill plan of the same tables
+ * reads them with d_out_indices as its kv_indices.  Rows of tokens that are
+ * not the plan's are left as they were.  Under PA_FLAG_CHECK_INDICES both
+ * index arrays are bounds-checked; tokens on a bad page are skipped. */
+pa_status pa_kv_read(pa_plan_t plan, const void* k_pool, const void* v_pool,
+                     const float* k_scales, const float* v_scales, const int32_t* d_kv_indices,
+                     void* k, int64_t k_stride, void* v, int64_t v_stride,
+                     const int32_t* d_out_indices, int64_t num_out_pages, void* d_workspace,
+                     size_t workspace_bytes, void* stream);
+
 /* Combine two attention states over disjoint token sets, row by row:
  *   M = max(lse_a, lse_b), w_x = exp(lse_x - M),
  *   o = (w_a o_a + w_b o_b) / (w_a + w_b),   lse = M + ln(w_a + w_b).

@@ -1,6 +1,6 @@
 // C-ABI entry points of libpagedattn.so that touch the device: workspace
-// upload, the run stage, cascade run, prefill run, merge_state, the index
-// check and the scheduling defaults.  Argument checking happens here, on the
+// upload, the run stage, cascade run, prefill run, cache write and read,
+// merge_state, the index check and the scheduling defaults.  Argument checking happens here, on the
 // host, before anything is enqueued; pointers must be device pointers
 // (16-byte aligned for q, o and the pools).
 #include <cuda_runtime.h>
@@ -33,6 +33,28 @@ pa_status check_run_args(pa_plan_t plan, const void* q, const void* k_pool, cons
   return PA_OK;
 }
 
+// Rows of k / v: 16-byte vectors, consecutive rows at least a row apart.
+bool rows_valid(const pa_plan_s& plan, const void* x, int64_t stride) {
+  return x && aligned16(x) && stride % 8 == 0 &&
+         stride >= int64_t(plan.prob.num_kv_heads) * plan.prob.head_dim;
+}
+
+pa_status check_kv_args(pa_plan_t plan, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, const void* k_pool, const void* v_pool,
+                        const float* k_scales, const float* v_scales, const int32_t* kv_indices,
+                        void* ws, size_t ws_bytes) {
+  if (!plan || !plan->kv_cache || !ws) return PA_ERR_INVALID_ARG;
+  if (ws_bytes < plan->ws.total) return PA_ERR_WORKSPACE_TOO_SMALL;
+  if (reinterpret_cast<uintptr_t>(ws) & (pa::kAlign - 1)) return PA_ERR_INVALID_ARG;
+  if (plan->total_q == 0) return PA_OK;
+  if (!rows_valid(*plan, k, k_stride) || !rows_valid(*plan, v, v_stride))
+    return PA_ERR_INVALID_ARG;
+  if (!k_pool || !v_pool || !aligned16(k_pool) || !aligned16(v_pool) || !k_scales || !v_scales ||
+      !kv_indices)
+    return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -56,8 +78,8 @@ pa_status pa_run(pa_plan_t plan, const void* q, const void* k_pool, const void* 
   pa_status st =
       check_run_args(plan, q, k_pool, v_pool, d_kv_indices, o, d_workspace, workspace_bytes);
   if (st != PA_OK) return st;
-  // cascade and prefill plans run through pa_cascade_run and pa_prefill_run
-  if (plan->cascade || plan->prefill) return PA_ERR_INVALID_ARG;
+  // other plans run through pa_cascade_run, pa_prefill_run, pa_kv_append / pa_kv_read
+  if (plan->cascade || plan->prefill || plan->kv_cache) return PA_ERR_INVALID_ARG;
   pa::RunPointers p{q, k_pool, v_pool, d_kv_indices, nullptr, o, lse,
                     static_cast<uint8_t*>(d_workspace)};
   return from_cuda(launch_decode_any(*plan, p, stream));
@@ -92,6 +114,40 @@ pa_status pa_prefill_run(pa_plan_t plan, const void* q, const void* k_pool, cons
   pa::RunPointers p{q, k_pool, v_pool, d_kv_indices, nullptr, o, lse,
                     static_cast<uint8_t*>(d_workspace)};
   return from_cuda(pa::launch_prefill(*plan, p, stream));
+}
+
+pa_status pa_kv_append(pa_plan_t plan, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, void* k_pool, void* v_pool, float* k_scales,
+                       float* v_scales, const int32_t* d_kv_indices, void* d_workspace,
+                       size_t workspace_bytes, void* stream) {
+  const pa_status st = check_kv_args(plan, k, k_stride, v, v_stride, k_pool, v_pool, k_scales,
+                                     v_scales, d_kv_indices, d_workspace, workspace_bytes);
+  if (st != PA_OK) return st;
+  const pa::KvPointers p{const_cast<void*>(k), const_cast<void*>(v), k_stride, v_stride,
+                         k_pool, v_pool, k_scales, v_scales, d_kv_indices, nullptr, 0,
+                         static_cast<uint8_t*>(d_workspace)};
+  return from_cuda(pa::launch_kv_append(*plan, p, stream));
+}
+
+pa_status pa_kv_read(pa_plan_t plan, const void* k_pool, const void* v_pool,
+                     const float* k_scales, const float* v_scales, const int32_t* d_kv_indices,
+                     void* k, int64_t k_stride, void* v, int64_t v_stride,
+                     const int32_t* d_out_indices, int64_t num_out_pages, void* d_workspace,
+                     size_t workspace_bytes, void* stream) {
+  const pa_status st = check_kv_args(plan, k, k_stride, v, v_stride, k_pool, v_pool, k_scales,
+                                     v_scales, d_kv_indices, d_workspace, workspace_bytes);
+  if (st != PA_OK) return st;
+  if (d_out_indices) {
+    const int64_t row = int64_t(plan->prob.num_kv_heads) * plan->prob.head_dim;
+    if (k_stride != row || v_stride != row || num_out_pages < 0) return PA_ERR_INVALID_ARG;
+    // pool rows are 32-bit indices inside the kernel
+    if (num_out_pages > int64_t(UINT32_MAX) / plan->prob.page_size) return PA_ERR_UNSUPPORTED;
+  }
+  const pa::KvPointers p{k, v, k_stride, v_stride, const_cast<void*>(k_pool),
+                         const_cast<void*>(v_pool), const_cast<float*>(k_scales),
+                         const_cast<float*>(v_scales), d_kv_indices, d_out_indices,
+                         num_out_pages, static_cast<uint8_t*>(d_workspace)};
+  return from_cuda(pa::launch_kv_read(*plan, p, stream));
 }
 
 pa_status pa_merge_state(const void* o_a, const float* lse_a, const void* o_b,

@@ -26,8 +26,9 @@ inline size_t align_up(size_t x, size_t a = kAlign) { return (x + a - 1) / a * a
 //                                      (prefill plans only)
 //   cta_indptr   [n_cta + 1]           int32, pieces (prefill: items) of CTA i
 //   merge_indptr [B * Hkv + 1]         int32, partial slots of segment (b, h)
-//   kv_len       [B]                   int32, tokens per request (rotary plans only:
-//                                      the query's position is kv_len - 1)
+//   kv_len       [B]                   int32, tokens per request (decode plans: the
+//                                      query's position is kv_len - 1)
+//   kv_spans     [n_spans]             pa::KvSpan (cache plans only)
 //   counters     [B * Hkv * kCounterSlots]  int32, zero between runs (decode levels only)
 //   error        [2]                   uint64: first bad kv_indices position (~0 = none),
 //                                      then a timeout flag (0 = none)
@@ -38,9 +39,18 @@ inline size_t align_up(size_t x, size_t a = kAlign) { return (x + a - 1) / a * a
 //                                      chunk's state of every row (normalised)
 //   prefix_lse   [prefix_chunks, B, Hq]     fp32, base 2 (cascade only)
 struct WorkspaceLayout {
-  size_t items = 0, prefill_tiles = 0, prefill_sched = 0, cta_indptr = 0, merge_indptr = 0, kv_len = 0, counters = 0,
-         error = 0, partial_o = 0, partial_lse = 0, prefix_o = 0, prefix_lse = 0, total = 0;
+  size_t items = 0, prefill_tiles = 0, prefill_sched = 0, cta_indptr = 0, merge_indptr = 0,
+         kv_len = 0, kv_spans = 0, counters = 0, error = 0, partial_o = 0, partial_lse = 0,
+         prefix_o = 0, prefix_lse = 0, total = 0;
 };
+
+// One run of a cache plan's tokens: request tokens [begin, end) of the span of
+// max(16, scale_block) tokens that starts at `start` (a multiple of its
+// length), in rows row, row + 1, ... of k and v.  Pages as in pa_work_item.
+struct KvSpan {
+  int32_t page_begin, start, begin, end, row;
+};
+constexpr int kKvSpanTokens = 16;  // fewest tokens of a span: one warp's rows
 
 }  // namespace pa
 
@@ -62,10 +72,15 @@ struct pa_plan_s {
   int32_t q_tiles = 0;              // 256-row CTA tiles over the B * G query rows of one kv head
   // prefill / append (pa_prefill_plan_create): query tiles, longest first
   bool prefill = false;
+  bool causal = false;
   int64_t total_q = 0;
   std::vector<int32_t> qo_indptr;
   std::vector<pa_prefill_tile> prefill_tiles;
   std::vector<int32_t> prefill_sched;  // items (tile * Hkv + kv head), grouped by CTA
+  // cache writes and reads (pa_kv_plan_create)
+  bool kv_cache = false;
+  int32_t scale_block = 0;
+  std::vector<pa::KvSpan> kv_spans;
   pa::WorkspaceLayout ws;
   // Bytes [0, ws.partial_o) of the workspace as pa_plan_upload writes them:
   // work list, CTA and merge offsets, zeroed counters and the status words
@@ -94,6 +109,10 @@ inline bool kv_is_8bit(const pa_problem& p) {
   return p.kv_dtype == PA_E4M3 || p.kv_dtype == PA_E5M2;
 }
 inline bool decode_needs_cuda_cores(const pa_problem& p) { return p.rope_theta > 0.f; }
+// Tokens per scale of a block-scaled cache: a power of two dividing the page.
+inline bool scale_block_valid(int32_t block, int32_t page_size) {
+  return block > 0 && (block & (block - 1)) == 0 && page_size % block == 0;
+}
 // Problems the CUDA-core kernel runs on its fp32 path (decode_f32.cu).
 inline bool decode_f32_path(const pa_problem& p) { return kv_is_8bit(p) || p.rope_theta > 0.f; }
 
@@ -134,6 +153,22 @@ int launch_prefill(const pa_plan_s& plan, const RunPointers& p, void* stream);
 int launch_merge_state(const void* o_a, const float* lse_a, const void* o_b, const float* lse_b,
                        void* o, float* lse, int64_t rows, int32_t head_dim, pa_dtype dtype,
                        void* stream);
+// Rows of a cache write (k, v) or read, and where a paged read goes.
+struct KvPointers {
+  void* k;
+  void* v;
+  int64_t k_stride, v_stride;  // elements between rows
+  void* k_pool;
+  void* v_pool;
+  float* k_scales;
+  float* v_scales;
+  const int32_t* kv_indices;
+  const int32_t* out_indices;
+  int64_t num_out_pages;
+  uint8_t* ws;
+};
+int launch_kv_append(const pa_plan_s& plan, const KvPointers& p, void* stream);
+int launch_kv_read(const pa_plan_s& plan, const KvPointers& p, void* stream);
 int decode_ctas_per_sm(int32_t group, pa_dtype dtype, int32_t* out);
 bool decode_group_supported(int32_t group);
 bool cascade_page_size_supported(int32_t page_size);

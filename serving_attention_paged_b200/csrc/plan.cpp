@@ -192,8 +192,10 @@ void layout_workspace(pa_plan_s* plan) {
   w.prefill_sched = take(plan->prefill_sched.size() * sizeof(int32_t));
   w.cta_indptr = take(plan->cta_indptr.size() * sizeof(int32_t));
   w.merge_indptr = take(plan->merge_indptr.size() * sizeof(int32_t));
-  w.kv_len = take(p.rope_theta > 0.f && !plan->prefill ? B * sizeof(int32_t) : 0);
-  w.counters = take(plan->prefill ? 0 : B * p.num_kv_heads * pa::kCounterSlots * sizeof(int32_t));
+  const bool decode = !plan->prefill && !plan->kv_cache;
+  w.kv_len = take(decode ? B * sizeof(int32_t) : 0);
+  w.kv_spans = take(plan->kv_spans.size() * sizeof(pa::KvSpan));
+  w.counters = take(!decode ? 0 : B * p.num_kv_heads * pa::kCounterSlots * sizeof(int32_t));
   w.error = take(2 * sizeof(uint64_t));  // first bad index, timeout flag
   const size_t G = plan->group;
   w.partial_o = take(size_t(plan->n_partials) * G * D * sizeof(float));
@@ -219,7 +221,10 @@ void build_upload_image(pa_plan_s* plan) {
               plan->cta_indptr.size() * sizeof(int32_t));
   std::memcpy(img.data() + w.merge_indptr, plan->merge_indptr.data(),
               plan->merge_indptr.size() * sizeof(int32_t));
-  if (plan->prob.rope_theta > 0.f && !plan->prefill) {
+  if (!plan->kv_spans.empty())
+    std::memcpy(img.data() + w.kv_spans, plan->kv_spans.data(),
+                plan->kv_spans.size() * sizeof(pa::KvSpan));
+  if (!plan->prefill && !plan->kv_cache) {
     const pa_problem& p = plan->prob;
     for (int32_t b = 0; b < p.batch; ++b) {
       const int64_t n = int64_t(plan->kv_indptr[b + 1]) - plan->kv_indptr[b];
@@ -350,15 +355,58 @@ pa_status build_prefill(pa_plan_s* plan, bool causal, const int32_t* qo, const i
   return PA_OK;
 }
 
-enum class Mode { kDecode, kCascade, kPrefill };
+// Cache plan: each request's last Q_b tokens cut at multiples of the span
+// length (a scale block, or 16 tokens of smaller blocks), so that every block
+// is one span's.
+pa_status build_kv(pa_plan_s* plan, const int32_t* qo, const int32_t* indptr,
+                   const int32_t* last) {
+  const pa_problem& p = plan->prob;
+  const int64_t B = p.batch, P = p.page_size;
+  const int64_t span = std::max<int64_t>(pa::kKvSpanTokens, plan->scale_block);
+  if (B > 0 && (!qo || !indptr || !last)) return PA_ERR_INVALID_ARG;
+  if ((qo && qo[0] != 0) || (indptr && indptr[0] != 0)) return PA_ERR_INVALID_ARG;
+  for (int64_t b = 0; b < B; ++b) {
+    if (indptr[b + 1] < indptr[b] || qo[b + 1] < qo[b]) return PA_ERR_INVALID_ARG;
+    const int64_t n = int64_t(indptr[b + 1]) - indptr[b];
+    if (n > 0 && (last[b] < 1 || last[b] > P)) return PA_ERR_INVALID_ARG;
+    const int64_t L = n > 0 ? (n - 1) * P + last[b] : 0;
+    if (L > INT32_MAX - 1024) return PA_ERR_UNSUPPORTED;  // span ends are 32-bit too
+    const int64_t first = L - (int64_t(qo[b + 1]) - qo[b]);
+    if (first < 0) return PA_ERR_INVALID_ARG;
+    for (int64_t s = first / span * span; s < L; s += span) {
+      const int64_t begin = std::max(s, first), end = std::min(s + span, L);
+      if (begin == end) continue;  // no tokens of this plan
+      plan->kv_spans.push_back(pa::KvSpan{indptr[b], int32_t(s), int32_t(begin), int32_t(end),
+                                          int32_t(qo[b] + (begin - first))});
+    }
+  }
+  plan->total_q = B > 0 ? qo[B] : 0;
+  if (B > 0) plan->kv_indptr.assign(indptr, indptr + B + 1);
+  else plan->kv_indptr.assign(1, 0);
+  plan->last_page_len.assign(last ? last : nullptr, last ? last + B : nullptr);
+  plan->cta_indptr.assign(1, 0);
+  plan->merge_indptr.assign(1, 0);
+  // one warp (or CTA) per span, kv head, and K and V; a grid's x extent is 2^31 - 1
+  const int64_t pieces = span / pa::kKvSpanTokens;
+  if (int64_t(plan->kv_spans.size()) > INT32_MAX / (2 * int64_t(p.num_kv_heads) * pieces))
+    return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+enum class Mode { kDecode, kCascade, kPrefill, kCache };
 
 pa_status create(const pa_problem* problem, int32_t prefix_len, Mode mode, bool causal,
-                 const int32_t* qo, const int32_t* indptr, const int32_t* last, pa_plan_t* out) {
+                 const int32_t* qo, const int32_t* indptr, const int32_t* last, pa_plan_t* out,
+                 int32_t scale_block = 0) {
   const bool cascade = mode == Mode::kCascade;
   if (!out) return PA_ERR_INVALID_ARG;
   *out = nullptr;
   pa_status st = validate_problem(problem);
   if (st != PA_OK) return st;
+  if (mode == Mode::kCache &&
+      (!pa::kv_is_8bit(*problem) || problem->k_scale != 1.f || problem->v_scale != 1.f ||
+       !pa::scale_block_valid(scale_block, problem->page_size)))
+    return PA_ERR_INVALID_ARG;
   if (cascade && (prefix_len < 0 || prefix_len % problem->page_size)) return PA_ERR_INVALID_ARG;
   // the prefix level and prefill read 16-bit pools with TMA, without rotation
   if (((cascade && prefix_len > 0) || mode == Mode::kPrefill) && pa::decode_f32_path(*problem))
@@ -378,8 +426,13 @@ pa_status create(const pa_problem* problem, int32_t prefix_len, Mode mode, bool 
     plan->log2_page = ilog2(problem->page_size);
     plan->cascade = cascade;
     plan->prefill = mode == Mode::kPrefill;
+    plan->causal = plan->prefill && causal;
+    plan->kv_cache = mode == Mode::kCache;
+    plan->scale_block = scale_block;
     plan->prefix_len = cascade ? prefix_len : 0;
-    st = plan->prefill ? build_prefill(plan, causal, qo, indptr, last) : build(plan, indptr, last);
+    st = plan->prefill    ? build_prefill(plan, causal, qo, indptr, last)
+         : plan->kv_cache ? build_kv(plan, qo, indptr, last)
+                          : build(plan, indptr, last);
     if (st == PA_OK) {
       if (cascade) schedule_prefix(plan);
       layout_workspace(plan);
@@ -418,6 +471,13 @@ pa_status pa_prefill_plan_create(const pa_problem* problem, int32_t causal,
                                  const int32_t* last_page_len_host, pa_plan_t* out) {
   return create(problem, 0, Mode::kPrefill, causal != 0, qo_indptr_host, kv_indptr_host,
                 last_page_len_host, out);
+}
+
+pa_status pa_kv_plan_create(const pa_problem* problem, int32_t scale_block,
+                            const int32_t* qo_indptr_host, const int32_t* kv_indptr_host,
+                            const int32_t* last_page_len_host, pa_plan_t* out) {
+  return create(problem, 0, Mode::kCache, false, qo_indptr_host, kv_indptr_host,
+                last_page_len_host, out, scale_block);
 }
 
 pa_status pa_plan_prefill_tiles(pa_plan_t plan, const pa_prefill_tile** tiles, int64_t* n_tiles) {
@@ -503,6 +563,7 @@ const char* pa_status_string(pa_status s) {
 
 int32_t pa_plan_uses_tensor_cores(pa_plan_t plan) {
   if (!plan) return -1;
+  if (plan->kv_cache) return 0;
   return plan->prefill ? 1 : int32_t(pa::decode_uses_tensor_cores(plan->prob));
 }
 

@@ -57,7 +57,7 @@ pa_status static_workspace_address(void** out) {
 extern "C" pa_status pa_run_static_workspace(pa_plan_t plan, const void* q, const void* k_pool,
                                              const void* v_pool, const int32_t* d_kv_indices,
                                              void* o, float* lse, void* stream) {
-  if (!plan || plan->cascade || plan->prefill) return PA_ERR_INVALID_ARG;
+  if (!plan || plan->cascade || plan->prefill || plan->kv_cache) return PA_ERR_INVALID_ARG;
   if (plan->ws.total > kStaticWorkspaceBytes) return PA_ERR_WORKSPACE_TOO_SMALL;
   void* ws = nullptr;
   pa_status st = static_workspace_address(&ws);
@@ -69,7 +69,7 @@ extern "C" pa_status pa_run_static_workspace(pa_plan_t plan, const void* q, cons
 
 extern "C" pa_status pa_static_workspace_check(pa_plan_t plan, int64_t* bad_position,
                                                void* stream) {
-  if (!plan || plan->cascade || plan->prefill) return PA_ERR_INVALID_ARG;
+  if (!plan || plan->cascade || plan->prefill || plan->kv_cache) return PA_ERR_INVALID_ARG;
   if (plan->ws.total > kStaticWorkspaceBytes) return PA_ERR_WORKSPACE_TOO_SMALL;
   void* ws = nullptr;
   const pa_status st = static_workspace_address(&ws);

@@ -53,6 +53,12 @@ class pa_prefill_tile(ctypes.Structure):
                 ("request", "q_begin", "n_q", "page_begin", "kv_base", "kv_end")]
 
 
+class pa_attention_options(ctypes.Structure):
+    _fields_ = [("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("scale_block", ctypes.c_int32), ("logit_cap", ctypes.c_float),
+                ("alibi_slopes", ctypes.c_void_p)]
+
+
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _P = ctypes.POINTER
 _SIGS = {
@@ -61,6 +67,9 @@ _SIGS = {
     "pa_prefill_plan_create": [_P(pa_problem), _i32, _vp, _vp, _vp, _P(_vp)],
     "pa_plan_prefill_tiles": [_vp, _P(_P(pa_prefill_tile)), _P(_i64)],
     "pa_prefill_run": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "pa_kv_plan_create": [_P(pa_problem), _i32, _vp, _vp, _vp, _P(_vp)],
+    "pa_kv_append": [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "pa_kv_read": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _sz, _vp],
     "pa_plan_quota_tokens": [_vp, _P(_i32)],
     "pa_plan_cta_indptr": [_vp, _P(_P(_i32)), _P(_i64)],
     "pa_plan_prefill_schedule": [_vp, _P(_P(_i32)), _P(_i64)],
@@ -191,6 +200,18 @@ def pa_prefill_plan_create(problem: pa_problem, causal: bool, qo_indptr_host, kv
     return Plan(h.value)
 
 
+def pa_kv_plan_create(problem: pa_problem, scale_block: int, qo_indptr_host, kv_indptr_host,
+                      last_page_len_host) -> Plan:
+    qo = _host_i32(qo_indptr_host)
+    indptr, last = _host_i32(kv_indptr_host), _host_i32(last_page_len_host)
+    h = _vp()
+    _check(lib.pa_kv_plan_create(ctypes.byref(problem), scale_block, qo.ctypes.data,
+                                 indptr.ctypes.data, last.ctypes.data if last.size else None,
+                                 ctypes.byref(h)),
+           "pa_kv_plan_create")
+    return Plan(h.value)
+
+
 def pa_plan_prefill_tiles(plan: Plan) -> np.ndarray:
     """The prefill tiles in launch order as an int32 array [n, 6] (a copy):
     request, q_begin, n_q, page_begin, kv_base, kv_end."""
@@ -296,6 +317,24 @@ def pa_prefill_run(plan: Plan, q, k_pool, v_pool, kv_indices, o, lse, workspace,
                               _ptr(o), _ptr(lse), _ptr(workspace), workspace_bytes,
                               _stream(stream)),
            "pa_prefill_run")
+
+
+def pa_kv_append(plan: Plan, k, k_stride: int, v, v_stride: int, k_pool, v_pool, k_scales,
+                 v_scales, kv_indices, workspace, workspace_bytes: int, stream=None):
+    _check(lib.pa_kv_append(plan.handle, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(k_pool),
+                            _ptr(v_pool), _ptr(k_scales), _ptr(v_scales), _ptr(kv_indices),
+                            _ptr(workspace), workspace_bytes, _stream(stream)),
+           "pa_kv_append")
+
+
+def pa_kv_read(plan: Plan, k_pool, v_pool, k_scales, v_scales, kv_indices, k, k_stride: int, v,
+               v_stride: int, out_indices, num_out_pages: int, workspace, workspace_bytes: int,
+               stream=None):
+    _check(lib.pa_kv_read(plan.handle, _ptr(k_pool), _ptr(v_pool), _ptr(k_scales),
+                          _ptr(v_scales), _ptr(kv_indices), _ptr(k), k_stride, _ptr(v), v_stride,
+                          _ptr(out_indices), num_out_pages, _ptr(workspace), workspace_bytes,
+                          _stream(stream)),
+           "pa_kv_read")
 
 
 def pa_run_static_workspace(plan: Plan, q, k_pool, v_pool, kv_indices, o, lse, stream=None):

@@ -2,8 +2,9 @@
 
 ``PagedDecode`` holds a plan and its device workspace (allocated through
 torch, the library itself never allocates) and calls ``pa_run`` /
-``pa_cascade_run``; ``PagedPrefill`` does the same for ``pa_prefill_run``.
-They only marshal arguments; all attention work is done by the library's
+``pa_cascade_run``; ``PagedPrefill`` does the same for ``pa_prefill_run`` and
+``PagedKV`` for ``pa_kv_append`` / ``pa_kv_read`` (8-bit caches with a scale
+for each block of tokens and kv head).  They only marshal arguments; all attention work is done by the library's
 kernels.
 """
 from __future__ import annotations
@@ -13,6 +14,22 @@ import torch
 from . import pagedattn as C
 
 _TORCH_DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
+
+
+_KV8_DTYPES = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+
+
+def _require(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _check_scales(scales, num_pages, page_size, num_kv_heads, scale_block, device, name):
+    _require(scales.dtype == torch.float32 and scales.device == device and scales.is_contiguous(),
+             f"{name}: a contiguous float32 tensor on {device}")
+    _require(scales.numel() == num_pages * page_size // scale_block * num_kv_heads,
+             f"{name}: one scale for each block of {scale_block} tokens and kv head "
+             f"([num_pages * page_size / scale_block, num_kv_heads])")
 
 
 class PagedDecode:
@@ -131,3 +148,118 @@ class PagedPrefill:
 
     def check(self, stream=None) -> int:
         return C.pa_plan_check(self.plan, self.workspace, stream)
+
+
+class PagedKV:
+    """Write and read back an 8-bit paged KV cache with one scale for each
+    block of ``scale_block`` tokens and kv head: plan once per batch of new
+    tokens (host), run once per layer (device).
+
+    The plan covers the last ``qo_indptr[b + 1] - qo_indptr[b]`` tokens of each
+    request, whose pages hold them already (lengths after the append).
+    ``scale_block`` is a power of two that divides the page (default: a page).
+    The pools are ``[num_pages, page_size, num_kv_heads, 128]`` codes
+    (``torch.float8_*`` or ``uint8``), the scales float32
+    ``[num_pages * page_size / scale_block, num_kv_heads]``; both are read by
+    ``PagedDecode.run(..., k_scales=, v_scales=, scale_block=)``.
+    """
+
+    def __init__(self, qo_indptr, kv_indptr, last_page_len, *, num_kv_heads, page_size, dtype,
+                 kv_dtype, num_pages, scale_block=None, head_dim=128, device=None, flags=0,
+                 stream=None):
+        self.device = torch.device(device if device is not None else "cuda")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.dtype, self.kv_dtype = dtype, kv_dtype
+        self.batch = len(last_page_len)
+        _require(len(qo_indptr) == self.batch + 1 and len(kv_indptr) == self.batch + 1,
+                 "qo_indptr and kv_indptr have batch + 1 entries")
+        self.total_q = int(qo_indptr[-1])
+        self.total_pages = int(kv_indptr[-1])
+        self.num_kv_heads, self.page_size, self.head_dim = num_kv_heads, page_size, head_dim
+        self.num_pages = num_pages
+        self.scale_block = page_size if scale_block is None else scale_block
+        self.problem = C.make_problem(batch=self.batch, num_qo_heads=num_kv_heads,
+                                      num_kv_heads=num_kv_heads, head_dim=head_dim,
+                                      page_size=page_size, dtype=dtype, sm_scale=1.0, num_sms=1,
+                                      ctas_per_sm=1, num_pages=num_pages, flags=flags,
+                                      kv_dtype=kv_dtype)
+        self.plan = C.pa_kv_plan_create(self.problem, self.scale_block, qo_indptr, kv_indptr,
+                                        last_page_len)
+        self.workspace_bytes = C.pa_plan_workspace_bytes(self.plan)
+        with torch.cuda.device(self.device):
+            self.workspace = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8,
+                                         device=self.device)
+            C.pa_plan_upload(self.plan, self.workspace, self.workspace.numel(), stream)
+
+    def _check_cache(self, k_pool, v_pool, k_scales, v_scales, kv_indices):
+        n = self.num_pages * self.page_size * self.num_kv_heads * self.head_dim
+        for name, pool in (("k_pool", k_pool), ("v_pool", v_pool)):
+            _require(pool.dtype in (torch.uint8, _KV8_DTYPES[self.kv_dtype])
+                     and pool.device == self.device and pool.is_contiguous()
+                     and pool.numel() == n,
+                     f"{name}: contiguous {self.kv_dtype} codes "
+                     "[num_pages, page_size, num_kv_heads, 128] on the plan's device")
+        for name, scales in (("k_scales", k_scales), ("v_scales", v_scales)):
+            _check_scales(scales, self.num_pages, self.page_size, self.num_kv_heads,
+                          self.scale_block, self.device, name)
+        self._check_indices(kv_indices, "kv_indices")
+
+    def _check_indices(self, indices, name):
+        _require(indices.dtype == torch.int32 and indices.device == self.device
+                 and indices.is_contiguous() and indices.numel() >= self.total_pages,
+                 f"{name}: contiguous int32, one entry per page of the plan")
+
+    def _check_rows(self, x, name):
+        _require(x.dtype == _TORCH_DTYPES[self.dtype] and x.device == self.device
+                 and x.shape == (self.total_q, self.num_kv_heads, self.head_dim)
+                 and x.stride(2) == 1 and x.stride(1) == self.head_dim,
+                 f"{name}: {self.dtype} rows [total_q, num_kv_heads, 128], heads packed")
+        # a single row has no next one to be apart from
+        return x.stride(0) if self.total_q > 1 else self.num_kv_heads * self.head_dim
+
+    def append(self, k, v, k_pool, v_pool, k_scales, v_scales, kv_indices, stream=None):
+        """Quantise the plan's tokens (``k``, ``v``: ``[total_q, num_kv_heads,
+        128]``, rows at any stride that is a multiple of 8) into the pools and
+        scales, in place."""
+        self._check_cache(k_pool, v_pool, k_scales, v_scales, kv_indices)
+        ks, vs = self._check_rows(k, "k"), self._check_rows(v, "v")
+        with torch.cuda.device(self.device):
+            C.pa_kv_append(self.plan, k, ks, v, vs, k_pool, v_pool, k_scales, v_scales,
+                           kv_indices, self.workspace, self.workspace.numel(), stream)
+
+    def read(self, k_pool, v_pool, k_scales, v_scales, kv_indices, k=None, v=None,
+             out_indices=None, stream=None):
+        """The plan's tokens in 16 bits: rows ``[total_q, num_kv_heads, 128]``,
+        or, with ``out_indices`` (a page of ``k`` / ``v`` for each of the
+        plan's pages), pages of the given 16-bit pools ``k`` and ``v``."""
+        self._check_cache(k_pool, v_pool, k_scales, v_scales, kv_indices)
+        row = self.num_kv_heads * self.head_dim
+        out_pages = 0
+        if out_indices is not None:
+            self._check_indices(out_indices, "out_indices")
+            shape = (self.page_size, self.num_kv_heads, self.head_dim)
+            for name, x in (("k", k), ("v", v)):
+                _require(x is not None and x.dtype == _TORCH_DTYPES[self.dtype]
+                         and x.device == self.device and x.is_contiguous() and x.dim() == 4
+                         and x.shape[1:] == shape,
+                         f"{name}: a contiguous {self.dtype} pool "
+                         "[pages, page_size, num_kv_heads, 128] to unpack into")
+            _require(k.shape == v.shape, "k and v pools of the same size")
+            ks = vs = row
+            out_pages = k.shape[0]
+        else:
+            shape = (self.total_q, self.num_kv_heads, self.head_dim)
+            if k is None:
+                k = torch.empty(shape, dtype=_TORCH_DTYPES[self.dtype], device=self.device)
+            if v is None:
+                v = torch.empty(shape, dtype=_TORCH_DTYPES[self.dtype], device=self.device)
+            ks, vs = self._check_rows(k, "k"), self._check_rows(v, "v")
+        with torch.cuda.device(self.device):
+            C.pa_kv_read(self.plan, k_pool, v_pool, k_scales, v_scales, kv_indices, k, ks, v, vs,
+                         out_indices, out_pages, self.workspace, self.workspace.numel(), stream)
+        return k, v
+
+    def check(self, stream=None) -> int:
+        with torch.cuda.device(self.device):
+            return C.pa_plan_check(self.plan, self.workspace, stream)
