@@ -33,6 +33,31 @@ pa_status check_run_args(pa_plan_t plan, const void* q, const void* k_pool, cons
   return PA_OK;
 }
 
+// What a run asks for: the options if they ask for anything, else null.
+const pa_attention_options* asked(const pa_attention_options* o) {
+  if (!o) return nullptr;
+  const bool nothing = !o->k_scales && !o->v_scales && o->logit_cap == 0.f && !o->alibi_slopes;
+  return nothing && o->scale_block == 0 ? nullptr : o;
+}
+
+pa_status check_options(const pa_plan_s& plan, const pa_attention_options& o) {
+  const pa_problem& pr = plan.prob;
+  if (o.logit_cap != 0.f && !(o.logit_cap >= 0x1p-20f && o.logit_cap <= 0x1p20f))
+    return PA_ERR_INVALID_ARG;  // NaN too
+  const auto misaligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; };
+  if (misaligned(o.k_scales) || misaligned(o.v_scales) || misaligned(o.alibi_slopes))
+    return PA_ERR_INVALID_ARG;
+  if (o.k_scales || o.v_scales || o.scale_block != 0) {
+    if (plan.prefill) return PA_ERR_UNSUPPORTED;
+    if (!pa::kv_is_8bit(pr) || !o.k_scales || !o.v_scales ||
+        !pa::scale_block_valid(o.scale_block, pr.page_size) || pr.k_scale != 1.f ||
+        pr.v_scale != 1.f)
+      return PA_ERR_INVALID_ARG;
+  }
+  if (plan.prefill && !plan.causal && o.alibi_slopes) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
 // Rows of k / v: 16-byte vectors, consecutive rows at least a row apart.
 bool rows_valid(const pa_plan_s& plan, const void* x, int64_t stride) {
   return x && aligned16(x) && stride % 8 == 0 &&
@@ -75,13 +100,23 @@ pa_status pa_plan_upload(pa_plan_t plan, void* d_workspace, size_t workspace_byt
 pa_status pa_run(pa_plan_t plan, const void* q, const void* k_pool, const void* v_pool,
                  const int32_t* d_kv_indices, void* o, float* lse, void* d_workspace,
                  size_t workspace_bytes, void* stream) {
+  return pa_run_options(plan, nullptr, q, k_pool, v_pool, d_kv_indices, o, lse, d_workspace,
+                        workspace_bytes, stream);
+}
+
+pa_status pa_run_options(pa_plan_t plan, const pa_attention_options* options, const void* q,
+                         const void* k_pool, const void* v_pool, const int32_t* d_kv_indices,
+                         void* o, float* lse, void* d_workspace, size_t workspace_bytes,
+                         void* stream) {
   pa_status st =
       check_run_args(plan, q, k_pool, v_pool, d_kv_indices, o, d_workspace, workspace_bytes);
   if (st != PA_OK) return st;
   // other plans run through pa_cascade_run, pa_prefill_run, pa_kv_append / pa_kv_read
   if (plan->cascade || plan->prefill || plan->kv_cache) return PA_ERR_INVALID_ARG;
   pa::RunPointers p{q, k_pool, v_pool, d_kv_indices, nullptr, o, lse,
-                    static_cast<uint8_t*>(d_workspace)};
+                    static_cast<uint8_t*>(d_workspace), asked(options)};
+  if (p.options) st = check_options(*plan, *p.options);
+  if (st != PA_OK) return st;
   return from_cuda(launch_decode_any(*plan, p, stream));
 }
 
@@ -107,12 +142,22 @@ pa_status pa_cascade_run(pa_plan_t plan, const void* q, const void* k_pool,
 pa_status pa_prefill_run(pa_plan_t plan, const void* q, const void* k_pool, const void* v_pool,
                          const int32_t* d_kv_indices, void* o, float* lse, void* d_workspace,
                          size_t workspace_bytes, void* stream) {
+  return pa_prefill_run_options(plan, nullptr, q, k_pool, v_pool, d_kv_indices, o, lse,
+                                d_workspace, workspace_bytes, stream);
+}
+
+pa_status pa_prefill_run_options(pa_plan_t plan, const pa_attention_options* options,
+                                 const void* q, const void* k_pool, const void* v_pool,
+                                 const int32_t* d_kv_indices, void* o, float* lse,
+                                 void* d_workspace, size_t workspace_bytes, void* stream) {
   pa_status st =
       check_run_args(plan, q, k_pool, v_pool, d_kv_indices, o, d_workspace, workspace_bytes);
   if (st != PA_OK) return st;
   if (!plan->prefill) return PA_ERR_INVALID_ARG;
   pa::RunPointers p{q, k_pool, v_pool, d_kv_indices, nullptr, o, lse,
-                    static_cast<uint8_t*>(d_workspace)};
+                    static_cast<uint8_t*>(d_workspace), asked(options)};
+  if (p.options) st = check_options(*plan, *p.options);
+  if (st != PA_OK) return st;
   return from_cuda(pa::launch_prefill(*plan, p, stream));
 }
 

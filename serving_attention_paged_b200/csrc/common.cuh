@@ -80,6 +80,12 @@ __device__ __forceinline__ void cp_async8_imm(uint32_t smem_addr, uint64_t gaddr
                "l"(gaddr), "r"(src_bytes), "n"(kDst), "n"(kSrc)
                : "memory");
 }
+// 4-byte form; src_bytes = 0 writes zero.
+__device__ __forceinline__ void cp_async4(uint32_t smem_addr, const void* gptr, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(smem_addr), "l"(gptr),
+               "r"(src_bytes)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;\n" ::: "memory");
 }

@@ -122,6 +122,7 @@ int decode_ctas_per_sm(int32_t group, pa_dtype dtype, int32_t* out) {
 
 int launch_decode(const pa_plan_s& plan, const RunPointers& p, void* stream) {
   const pa_problem& pr = plan.prob;
+  if (p.options) return launch_decode_options(plan, p, stream);
   DecodeArgs a;
   fill_decode_args(plan, p, &a);
   if (decode_f32_path(pr)) return launch_decode_f32(plan, a, stream);

@@ -1,7 +1,7 @@
 // The CUDA-core paged decode kernel, as a template shared by decode.cu
-// (16-bit pools, the mixed-precision path) and decode_f32.cu (8-bit pools
-// and rotary positions, the fp32 path).  The design is described at the top
-// of decode.cu.
+// (16-bit pools, the mixed-precision path), decode_f32.cu (8-bit pools
+// and rotary positions, the fp32 path) and decode_options.cu (either with
+// options: kExt).  The design is described at the top of decode.cu.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -12,6 +12,7 @@
 #include "common.cuh"
 #include "launch.cuh"
 #include "pa_internal.h"
+#include "score.cuh"
 
 namespace pa {
 namespace dec {
@@ -104,6 +105,11 @@ struct DecodeArgs {
   float score_scale;              // sm_scale * log2(e) (* k_scale for 8-bit pools)
   float v_scale;                  // 8-bit pools: value = v_scale * code
   float rope_hi[64], rope_lo[64]; // rotary: theta^(-d/64) / (2 pi) = hi + lo
+  // options (kExt)
+  const float* k_scales;          // block scales [num_pages * P >> log2_block, Hkv], or null
+  const float* v_scales;
+  int32_t log2_block;
+  ScoreArgs score;
 };
 
 // p as the PV step consumes it: fp16 for fp16 inputs, fp32 for bf16 (and on
@@ -168,11 +174,11 @@ __device__ __forceinline__ void pv_update(F16, const uint4& x, int v, const uint
     for (int i = 0; i < 4; ++i)
       axpy2_f16(p[hh], w[i], o[hh][8 * v + 2 * i], o[hh][8 * v + 2 * i + 1]);
 }
-template <int G, int E>
-__device__ __forceinline__ void pv_update(BF16, const uint4& x, int v, const float (&p)[G],
+template <typename Tag, int G, int E>
+__device__ __forceinline__ void pv_update(Tag, const uint4& x, int v, const float (&p)[G],
                                           float (&o)[G][E]) {
   float vf[8];
-  to_float8(BF16{}, x, vf);
+  to_float8(Tag{}, x, vf);
 #pragma unroll
   for (int hh = 0; hh < G; ++hh)
 #pragma unroll
@@ -297,18 +303,20 @@ __device__ __forceinline__ void copy_row(uint32_t dst, uint64_t ka, uint64_t va,
 // piece.  Addresses are formed with one 32x32->64-bit multiply-add per row
 // (pool row index x bytes per pool row + this lane's base); the V blocks and
 // the further blocks of a row use immediate offsets.
-template <typename C, int kCheckMode>
+// With block scales (kScaled and a.k_scales) the first lane of a token also
+// copies the token's K and V scale, into scale_ring [stage][K, V][kTile].
+template <typename C, int kCheckMode, bool kScaled>
 struct PieceCopier {
   static constexpr int TPG = C::TPG, kTile = C::kTile, kGroups = C::kGroups;
   static constexpr int kRowBytes = C::kRowBytes, kBlock = C::kBlockBytes;
   const DecodeArgs& a;
   const int32_t* page_list;
   uint64_t kaddr0, vaddr0;
-  uint32_t my_slot, pool_row_bytes, pmask;
-  int tb, len, ntiles, grp, lp, page_begin;
-  bool check;
+  uint32_t my_slot, pool_row_bytes, pmask, scale_slot;
+  int tb, len, ntiles, grp, lp, page_begin, kv_head;
+  bool check, copies_scales;
   __device__ __forceinline__ PieceCopier(const DecodeArgs& a_, const pa_work_item& it,
-                                         uint8_t* smem)
+                                         uint8_t* smem, const float* scale_ring)
       : a(a_) {
     const int tid = threadIdx.x;
     const int lt = tid & (C::LT - 1);
@@ -325,6 +333,11 @@ struct PieceCopier {
     page_begin = it.page_begin;
     page_list = a.kv_indices + it.page_begin;
     my_slot = smem_u32(smem) + grp * kRowBytes + lt * kBlock;
+    if constexpr (kScaled) {
+      kv_head = it.kv_head;
+      scale_slot = smem_u32(scale_ring) + grp * 4;
+      copies_scales = a.k_scales && lt == 0;
+    }
   }
   __device__ __forceinline__ void load_pages(int tile, int (&pg)[TPG]) const {
 #pragma unroll
@@ -343,6 +356,18 @@ struct PieceCopier {
     }
   }
   __device__ __forceinline__ void issue(int tile, uint32_t stage_off, const int (&pg)[TPG]) const {
+    if (kScaled && copies_scales && tile < ntiles) {
+      const uint32_t slot = scale_slot + stage_off / C::kStageBytes * (2 * kTile * 4);
+#pragma unroll
+      for (int j = 0; j < TPG; ++j) {
+        const uint32_t pos = uint32_t(tb + tile * kTile + grp + kGroups * j);
+        const bool ok = pg[j] >= 0;
+        const uint32_t row = ok ? ((uint32_t(pg[j]) << lp) | (pos & pmask)) : 0u;
+        const int64_t at = int64_t(row >> a.log2_block) * a.num_kv_heads + kv_head;
+        cp_async4(slot + j * kGroups * 4, a.k_scales + at, ok ? 4u : 0u);
+        cp_async4(slot + (kTile + j * kGroups) * 4, a.v_scales + at, ok ? 4u : 0u);
+      }
+    }
     if (tile < ntiles) {
 #pragma unroll
       for (int j = 0; j < TPG; ++j) {
@@ -374,18 +399,20 @@ struct PieceCopier {
 // `started` its first tiles are already being copied (by the previous piece,
 // which left tile kStages - 1's pages in pg); `next` (or null) is the CTA's
 // next piece, whose first copies this piece starts right after its last tile.
-template <typename Tag, typename KV, int G, int kCheckMode, bool kRope>
+template <typename Tag, typename KV, int G, int kCheckMode, bool kRope, bool kExt>
 __device__ __forceinline__ void run_piece(const DecodeArgs& a, const pa_work_item& it,
                                           const pa_work_item* next, bool started,
                                           int (&pg)[Cfg<G, KVBytes<KV>::v,
                                                         !std::is_same<KV, KV16>::value || kRope,
                                                         kRope>::TPG],
                                           uint8_t* smem, const float* rope_tab,
-                                          int& s_is_last) {
+                                          const float* scale_ring, int& s_is_last) {
   constexpr bool k8 = !std::is_same<KV, KV16>::value;
   constexpr bool kF32 = k8 || kRope;  // the fp32 path
+  constexpr bool kScaled = k8 && kExt;  // the pools may have block scales
   using C = Cfg<G, KVBytes<KV>::v, kF32, kRope>;
-  using PT = std::conditional_t<kF32, float, typename PType<Tag>::T>;
+  // with options P stays fp32 (l sums it as it is, so o and lse carry no rounding of it)
+  using PT = std::conditional_t<kF32 || kExt, float, typename PType<Tag>::T>;
   constexpr int LT = C::LT, E = C::E, V = C::V, TPG = C::TPG;
   constexpr int kGroups = C::kGroups, kTile = C::kTile;
   constexpr int kRowBytes = C::kRowBytes, kBlock = C::kBlockBytes;
@@ -477,8 +504,17 @@ __device__ __forceinline__ void run_piece(const DecodeArgs& a, const pa_work_ite
 
   // ---- loads: this thread's blocks of its TPG rows per tile ----
   constexpr int kStages = C::kStages;
-  const PieceCopier<C, kCheckMode> cp(a, it, smem);
+  const PieceCopier<C, kCheckMode, kScaled> cp(a, it, smem, scale_ring);
   if (!started) cp.start(pg);
+  // options: this lane's head's bias per unit of distance, the query's position
+  float slope2 = 0.f;
+  int qpos = 0;
+  if constexpr (kExt) {
+    if (a.score.slopes) {
+      slope2 = __ldg(a.score.slopes + hq0 + my_head) * kLog2e;
+      qpos = __ldg(a.kv_len + b) - 1;
+    }
+  }
 
   uint32_t issue_off = (kStages - 1) * C::kStageBytes;  // ring slot of tile t + kStages - 1
   uint32_t read_off = 0;                                 // ring slot of tile t
@@ -487,6 +523,16 @@ __device__ __forceinline__ void run_piece(const DecodeArgs& a, const pa_work_ite
     cp.load_pages(t + kStages, pg);
     issue_off = issue_off + C::kStageBytes == C::kRingBytes ? 0u : issue_off + C::kStageBytes;
     cp_async_wait<kStages - 1>();
+    float kscale[TPG], vscale[TPG];
+    if constexpr (kScaled) {
+      __syncwarp();  // the scales came with the token's first lane's copies
+      const float* sc = scale_ring + read_off / C::kStageBytes * (2 * kTile) + grp;
+#pragma unroll
+      for (int j = 0; j < TPG; ++j) {
+        kscale[j] = a.k_scales ? sc[j * kGroups] : 1.f;
+        vscale[j] = a.k_scales ? sc[kTile + j * kGroups] : 1.f;
+      }
+    }
     const uint8_t* ks = smem + read_off + grp * kRowBytes + lt * kBlock;
     read_off = read_off + C::kStageBytes == C::kRingBytes ? 0u : read_off + C::kStageBytes;
     const uint8_t* vs = ks + C::kHalfStage;
@@ -528,8 +574,13 @@ __device__ __forceinline__ void run_piece(const DecodeArgs& a, const pa_work_ite
           }
         }
       }
-      const float r = reduce_scatter<G, LT>(part);
-      sc[j] = (t * kTile + grp + kGroups * j < len) ? r * a.score_scale : -INFINITY;
+      float r = reduce_scatter<G, LT>(part) * a.score_scale;
+      if constexpr (kExt) {
+        if constexpr (kScaled) r *= kscale[j];
+        const float dist = float(qpos - (tb + t * kTile + grp + kGroups * j));
+        r = final_score(r, a.score, slope2, dist);
+      }
+      sc[j] = (t * kTile + grp + kGroups * j < len) ? r : -INFINITY;
     }
 
     // Lazy running max: the reference point m moves only when a score beats
@@ -550,6 +601,8 @@ __device__ __forceinline__ void run_piece(const DecodeArgs& a, const pa_work_ite
       if constexpr (sizeof(PT) == 2) {
         ps = __half_as_ushort(__float2half_rn(p));
         p = __half2float(__ushort_as_half(ps));  // l sums exactly what PV multiplies
+      } else if constexpr (kScaled) {
+        ps = p * vscale[j];
       } else {
         ps = p;
       }
@@ -590,7 +643,7 @@ __device__ __forceinline__ void run_piece(const DecodeArgs& a, const pa_work_ite
           }
         } else {
           const uint4 x = *reinterpret_cast<const uint4*>(vs + j * kGroups * kRowBytes + v * LT * 16);
-          pv_update<G, E>(Tag{}, x, v, pj, o);
+          pv_update(Tag{}, x, v, pj, o);
         }
       }
     }
@@ -599,7 +652,7 @@ __device__ __forceinline__ void run_piece(const DecodeArgs& a, const pa_work_ite
   // This thread's ring slots are free: start the next piece's copies, so they
   // land while this piece is combined and written.
   if (next) {
-    const PieceCopier<C, kCheckMode> np(a, *next, smem);
+    const PieceCopier<C, kCheckMode, kScaled> np(a, *next, smem, scale_ring);
     np.start(pg);
   }
 
@@ -751,13 +804,14 @@ template <typename KV, bool kRope> struct Path {
 template <typename Tag, typename KV, int G, int kCheckMode, bool kRope>
 using KCfg = Cfg<G, KVBytes<KV>::v, Path<KV, kRope>::kF32, kRope>;
 
-template <typename Tag, typename KV, int G, int kCheckMode, bool kRope>
+template <typename Tag, typename KV, int G, int kCheckMode, bool kRope, bool kExt>
 __global__ void __launch_bounds__(kThreads, (KCfg<Tag, KV, G, kCheckMode, kRope>::MINB))
     paged_decode_kernel(const DecodeArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_is_last;
   using C = KCfg<Tag, KV, G, kCheckMode, kRope>;
   float* rope_tab = reinterpret_cast<float*>(smem + C::kSmemBytes);
+  float* scale_ring = rope_tab + (kRope ? kRopeTableBytes / 4 : 0);  // options of 8-bit pools
   if constexpr (kRope) {
     rope_tab[threadIdx.x] = threadIdx.x < 64 ? a.rope_hi[threadIdx.x] : a.rope_lo[threadIdx.x - 64];
     __syncthreads();
@@ -766,21 +820,24 @@ __global__ void __launch_bounds__(kThreads, (KCfg<Tag, KV, G, kCheckMode, kRope>
   int pg[C::TPG];  // tile kStages - 1's pages of a piece whose copies are started
   for (int pi = p0; pi < p1; ++pi) {
     if (pi > p0) __syncthreads();  // the previous piece is done with p and the combine region
-    run_piece<Tag, KV, G, kCheckMode, kRope>(a, a.items[pi], pi + 1 < p1 ? a.items + pi + 1 : nullptr,
-                                             pi > p0, pg, smem, rope_tab, s_is_last);
+    run_piece<Tag, KV, G, kCheckMode, kRope, kExt>(
+        a, a.items[pi], pi + 1 < p1 ? a.items + pi + 1 : nullptr, pi > p0, pg, smem, rope_tab,
+        scale_ring, s_is_last);
   }
 }
 
-template <typename Tag, typename KV, int G, int kCheckMode, bool kRope>
+template <typename Tag, typename KV, int G, int kCheckMode, bool kRope, bool kExt>
 constexpr int smem_bytes() {
-  return KCfg<Tag, KV, G, kCheckMode, kRope>::kSmemBytes + (kRope ? kRopeTableBytes : 0);
+  using C = KCfg<Tag, KV, G, kCheckMode, kRope>;
+  const int scales = kExt && !std::is_same<KV, KV16>::value ? C::kStages * 2 * C::kTile * 4 : 0;
+  return C::kSmemBytes + (kRope ? kRopeTableBytes : 0) + scales;
 }
 
 // Resident CTAs per SM of one instantiation.
 template <typename Tag, typename KV, int G, int kCheckMode, bool kRope>
 cudaError_t occupancy_t(int* out) {
-  auto kern = paged_decode_kernel<Tag, KV, G, kCheckMode, kRope>;
-  constexpr int smem = smem_bytes<Tag, KV, G, kCheckMode, kRope>();
+  auto kern = paged_decode_kernel<Tag, KV, G, kCheckMode, kRope, false>;
+  constexpr int smem = smem_bytes<Tag, KV, G, kCheckMode, kRope, false>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, kern, kThreads, smem);
@@ -796,15 +853,15 @@ cudaError_t occupancy_group(int group, int* out) {
   return cudaErrorInvalidValue;
 }
 
-template <typename Tag, typename KV, int G, int kCheckMode, bool kRope>
+template <typename Tag, typename KV, int G, int kCheckMode, bool kRope, bool kExt>
 cudaError_t launch_t(const DecodeArgs& a, int64_t n_cta, cudaStream_t stream, bool pdl) {
-  auto kern = paged_decode_kernel<Tag, KV, G, kCheckMode, kRope>;
+  auto kern = paged_decode_kernel<Tag, KV, G, kCheckMode, kRope, kExt>;
   static std::atomic<uint64_t> configured{0};  // bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = uint64_t(1) << (dev & 63);
-  constexpr int kSmem = smem_bytes<Tag, KV, G, kCheckMode, kRope>();
+  constexpr int kSmem = smem_bytes<Tag, KV, G, kCheckMode, kRope, kExt>();
   if (!(configured.load() & bit)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
@@ -814,14 +871,14 @@ cudaError_t launch_t(const DecodeArgs& a, int64_t n_cta, cudaStream_t stream, bo
   return launch_maybe_dependent(kern, dim3(unsigned(n_cta)), dim3(kThreads), kSmem, stream, pdl, a);
 }
 
-template <typename Tag, typename KV, int kCheckMode, bool kRope>
+template <typename Tag, typename KV, int kCheckMode, bool kRope, bool kExt = false>
 cudaError_t dispatch_group(int group, const DecodeArgs& a, int64_t n, cudaStream_t s,
                            bool pdl = false) {
   switch (group) {
-    case 1: return launch_t<Tag, KV, 1, kCheckMode, kRope>(a, n, s, pdl);
-    case 2: return launch_t<Tag, KV, 2, kCheckMode, kRope>(a, n, s, pdl);
-    case 4: return launch_t<Tag, KV, 4, kCheckMode, kRope>(a, n, s, pdl);
-    case 8: return launch_t<Tag, KV, 8, kCheckMode, kRope>(a, n, s, pdl);
+    case 1: return launch_t<Tag, KV, 1, kCheckMode, kRope, kExt>(a, n, s, pdl);
+    case 2: return launch_t<Tag, KV, 2, kCheckMode, kRope, kExt>(a, n, s, pdl);
+    case 4: return launch_t<Tag, KV, 4, kCheckMode, kRope, kExt>(a, n, s, pdl);
+    case 8: return launch_t<Tag, KV, 8, kCheckMode, kRope, kExt>(a, n, s, pdl);
   }
   return cudaErrorInvalidValue;
 }

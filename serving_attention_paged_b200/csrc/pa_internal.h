@@ -101,6 +101,7 @@ struct RunPointers {
   void* o;
   float* lse;
   uint8_t* ws;
+  const pa_attention_options* options = nullptr;  // null: none
 };
 
 // 8-bit (FP8) KV cache (both decode kernels); rotary positions on the fly
@@ -120,6 +121,9 @@ int launch_decode(const pa_plan_s& plan, const RunPointers& p, void* stream);
 // Resident CTAs per SM of the fp32-path kernel (8-bit pools, rotary) a problem runs.
 int decode_f32_ctas_per_sm(const pa_problem& p, int32_t* out);
 int launch_decode_tc(const pa_plan_s& plan, const RunPointers& p, void* stream);
+// Either kernel's launches with options (p.options).
+int launch_decode_options(const pa_plan_s& plan, const RunPointers& p, void* stream);
+int launch_decode_tc_options(const pa_plan_s& plan, const RunPointers& p, void* stream);
 bool decode_tc_supported(int32_t group, pa_dtype dtype);
 int decode_tc_ctas_per_sm(int32_t group, pa_dtype dtype, int32_t* out);
 // The decode kernel a problem runs: the caller's choice if any, else tensor

@@ -56,6 +56,12 @@
 // without tiles), so the next item's Q loads and its first S runs while the
 // epilogue reads O.  Each half stages
 // its o rows in a 16 KB region of its own, 64 columns at a time.
+// Options (kExt; pa_prefill_run_options): the softmax warps turn the raw scores
+// into final base-2 scores as they are read.  A cap costs a polynomial of
+// tanh on the FMA pipe (score.cuh) while every |s| of a warp's tile is below
+// the cap, two MUFU operations per score in the rare tile where one is not;
+// the distance bias one FMA and one addition.  With a bias the tile maximum is
+// taken before the exponentials: the bias makes it grow from tile to tile.
 // Every mbarrier wait is bounded; on a timeout the kernel records it in the
 // workspace status word and unwinds instead of hanging.  Every parity wait
 // targets a barrier whose previous phase the waiting thread has itself
@@ -70,6 +76,7 @@
 #include "attn_tile.cuh"
 #include "common.cuh"
 #include "pa_internal.h"
+#include "score.cuh"
 #include "tcgen05.cuh"
 
 namespace pa {
@@ -130,8 +137,14 @@ struct PrefillArgs {
   int64_t num_pages;
   int32_t num_qo_heads, num_kv_heads, group, page_size, log2_page, box_rows;
   int32_t oob_row;                  // a pool row past the end (TMA zero fill)
-  float score_scale;                // sm_scale * log2(e)
+  float score_scale;                // sm_scale * log2(e), or as ScoreArgs has it
+  int32_t check;                    // options: bounds-check page indices
+  ScoreArgs score;                  // options
 };
+
+// Plain runs (index check off or on), or a run with options (the check is a
+// launch argument).
+enum PrefillMode { kPlain = 0, kChecked = 1, kOptions = 2 };
 
 __device__ __forceinline__ void flag_timeout(const PrefillArgs& a) {
   atomicOr(a.error_pos + 1, 1ull);
@@ -184,12 +197,14 @@ __device__ __forceinline__ Item load_item(const PrefillArgs& a, int j) {
   return it;
 }
 
-template <typename Tag, bool kCheck>
+template <typename Tag, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tmap_q,
                          const __grid_constant__ CUtensorMap tmap_k,
                          const __grid_constant__ CUtensorMap tmap_v, const PrefillArgs a) {
   constexpr bool kSplit = std::is_same<Tag, BF16>::value;
+  constexpr bool kExt = kMode == kOptions;
+  const bool check = kExt ? a.check != 0 : kMode == kChecked;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -253,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (key >= it.kv_end) return a.oob_row;
         const int pos = it.page_begin + (key >> a.log2_page);
         const int page = __ldg(a.kv_indices + pos);
-        if (kCheck && (page < 0 || int64_t(page) >= a.num_pages)) {
+        if (check && (page < 0 || int64_t(page) >= a.num_pages)) {
           atomicMin(a.error_pos, (unsigned long long)pos);
           return a.oob_row;  // read as zeros
         }
@@ -441,6 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t sc = 0, od = 0;  // S and O-done barrier phases this half has consumed
     for (int j = j0; j < j1; ++j) {
       int nt, lim, lim_min;
+      float slope2 = 0.f;  // options: bias per unit of distance, the row's position
+      int qpos = 0;
       {
         const Item it = load_item(a, j);
         nt = hf ? it.nt1 : it.nt0;
@@ -448,6 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // keys), and the fewest any row of the half sees
         lim = min(it.kv_base + jq + 1, it.kv_end);
         lim_min = min(it.kv_base + hf * per_half + 1, it.kv_end);
+        if constexpr (kExt) {
+          if (a.score.slopes) slope2 = __ldg(a.score.slopes + it.h * G + jh) * kLog2e;
+          qpos = it.kv_base + jq;
+        }
       }
       float m = -INFINITY, l = 0.f;
       bool ok = true;
@@ -469,6 +490,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         // stale row may be anything); tiles wholly below every row's limit need
         // no mask (uniform branch).
         const int key0 = kt * kKeys;
+        if constexpr (kExt) {
+          const float2 sc2 = make_float2(a.score_scale, a.score_scale);
+          if (a.score.cap_out > 0.f) {
+            // scores as fractions of the cap, then cap_out * tanh
+            float umax = 0.f;
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 2) {
+              const float2 y = __fmul2_rn(make_float2(x[c], x[c + 1]), sc2);
+              x[c] = y.x;
+              x[c + 1] = y.y;
+              umax = max3(umax, fabsf(y.x), fabsf(y.y));
+            }
+            if (__any_sync(0xffffffffu, !(umax <= 1.f))) {
+#pragma unroll
+              for (int c = 0; c < kKeys; ++c) x[c] = a.score.cap_out * tanh_score(x[c]);
+            } else {
+#pragma unroll
+              for (int c = 0; c < kKeys; c += 2) {
+                const float2 t = tanh_poly2(make_float2(x[c], x[c + 1]));
+                x[c] = a.score.cap_out * t.x;
+                x[c + 1] = a.score.cap_out * t.y;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 2) {
+              const float2 y = __fmul2_rn(make_float2(x[c], x[c + 1]), sc2);
+              x[c] = y.x;
+              x[c + 1] = y.y;
+            }
+          }
+          if (a.score.slopes) {
+            // -slope2 * (qpos - (key0 + c)), the distance of key0 first
+            const float b0 = -slope2 * float(qpos - key0);
+            const float2 s2 = make_float2(slope2, slope2), b2 = make_float2(b0, b0);
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 2) {
+              const float2 y = __fadd2_rn(make_float2(x[c], x[c + 1]),
+                                          __ffma2_rn(s2, make_float2(float(c), float(c + 1)), b2));
+              x[c] = y.x;
+              x[c + 1] = y.y;
+            }
+          }
+        }
         const bool masked = key0 + kKeys > lim_min;
         if (masked) {
 #pragma unroll
@@ -484,7 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const int c = 32 * c16 + 2 * e;
-              const float2 a2 = __ffma2_rn(make_float2(x[c], x[c + 1]), sc2, nm2);
+              const float2 a2 = kExt ? __fadd2_rn(make_float2(x[c], x[c + 1]), nm2)
+                                     : __ffma2_rn(make_float2(x[c], x[c + 1]), sc2, nm2);
               float2 p2;
               if (poly && (e & 7) < kPolyPairsPer8) {  // on the FMA pipe
                 p2 = exp2_poly2<kSplit ? 4 : 3>(a2);
@@ -518,10 +584,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             t2 = max3(t2, x[c + 2], x[c + 6]);
             t3 = max3(t3, x[c + 3], x[c + 7]);
           }
-          return max3(t0, t1, fmaxf(t2, t3)) * a.score_scale;
+          return max3(t0, t1, fmaxf(t2, t3)) * (kExt ? 1.f : a.score_scale);
         };
         float psum, alpha = 1.f;
-        if (kt == 0 || masked) {
+        if (kt == 0 || masked || (kExt && a.score.slopes)) {
           const float tmax = tile_max();
           const bool moved = tmax > m + kSlack;
           const float mnew = moved ? tmax : m;
@@ -650,10 +716,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-template <typename Tag, bool kCheck>
+template <typename Tag, int kMode>
 cudaError_t launch_t(const PrefillArgs& args, const CUtensorMap& tq, const CUtensorMap& tk,
                      const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  auto kern = paged_prefill_kernel<Tag, kCheck>;
+  auto kern = paged_prefill_kernel<Tag, kMode>;
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -710,11 +776,17 @@ int launch_prefill(const pa_plan_s& plan, const RunPointers& p, void* stream) {
   if (grid <= 0) return 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool check = (pr.flags & PA_FLAG_CHECK_INDICES) != 0;
+  if (p.options) {
+    a.check = check;
+    set_score_args(*p.options, &a.score, &a.score_scale);
+    return int(pr.dtype == PA_BF16 ? launch_t<BF16, kOptions>(a, tq, tk, tv, grid, s)
+                                   : launch_t<F16, kOptions>(a, tq, tk, tv, grid, s));
+  }
   if (pr.dtype == PA_BF16)
-    return int(check ? launch_t<BF16, true>(a, tq, tk, tv, grid, s)
-                     : launch_t<BF16, false>(a, tq, tk, tv, grid, s));
-  return int(check ? launch_t<F16, true>(a, tq, tk, tv, grid, s)
-                   : launch_t<F16, false>(a, tq, tk, tv, grid, s));
+    return int(check ? launch_t<BF16, kChecked>(a, tq, tk, tv, grid, s)
+                     : launch_t<BF16, kPlain>(a, tq, tk, tv, grid, s));
+  return int(check ? launch_t<F16, kChecked>(a, tq, tk, tv, grid, s)
+                   : launch_t<F16, kPlain>(a, tq, tk, tv, grid, s));
 }
 
 }  // namespace pa

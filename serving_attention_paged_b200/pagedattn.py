@@ -67,6 +67,9 @@ _SIGS = {
     "pa_prefill_plan_create": [_P(pa_problem), _i32, _vp, _vp, _vp, _P(_vp)],
     "pa_plan_prefill_tiles": [_vp, _P(_P(pa_prefill_tile)), _P(_i64)],
     "pa_prefill_run": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "pa_run_options": [_vp, _P(pa_attention_options), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "pa_prefill_run_options": [_vp, _P(pa_attention_options), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                               _sz, _vp],
     "pa_kv_plan_create": [_P(pa_problem), _i32, _vp, _vp, _vp, _P(_vp)],
     "pa_kv_append": [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
     "pa_kv_read": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _sz, _vp],
@@ -317,6 +320,29 @@ def pa_prefill_run(plan: Plan, q, k_pool, v_pool, kv_indices, o, lse, workspace,
                               _ptr(o), _ptr(lse), _ptr(workspace), workspace_bytes,
                               _stream(stream)),
            "pa_prefill_run")
+
+
+def make_options(*, k_scales=None, v_scales=None, scale_block=0, logit_cap=0.0,
+                 alibi_slopes=None) -> pa_attention_options:
+    """Options of one run; the arrays must outlive it."""
+    return pa_attention_options(_ptr(k_scales), _ptr(v_scales), scale_block, logit_cap,
+                                _ptr(alibi_slopes))
+
+
+def pa_run_options(plan: Plan, options: pa_attention_options, q, k_pool, v_pool, kv_indices, o,
+                   lse, workspace, workspace_bytes: int, stream=None):
+    _check(lib.pa_run_options(plan.handle, ctypes.byref(options), _ptr(q), _ptr(k_pool),
+                              _ptr(v_pool), _ptr(kv_indices), _ptr(o), _ptr(lse),
+                              _ptr(workspace), workspace_bytes, _stream(stream)),
+           "pa_run_options")
+
+
+def pa_prefill_run_options(plan: Plan, options: pa_attention_options, q, k_pool, v_pool,
+                           kv_indices, o, lse, workspace, workspace_bytes: int, stream=None):
+    _check(lib.pa_prefill_run_options(plan.handle, ctypes.byref(options), _ptr(q), _ptr(k_pool),
+                                      _ptr(v_pool), _ptr(kv_indices), _ptr(o), _ptr(lse),
+                                      _ptr(workspace), workspace_bytes, _stream(stream)),
+           "pa_prefill_run_options")
 
 
 def pa_kv_append(plan: Plan, k, k_stride: int, v, v_stride: int, k_pool, v_pool, k_scales,

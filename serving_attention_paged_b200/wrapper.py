@@ -19,6 +19,14 @@ _TORCH_DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
 _KV8_DTYPES = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 
 
+def _device(device) -> torch.device:
+    """The given device (default: the current one), with its index."""
+    device = torch.device(device if device is not None else "cuda")
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
 def _require(ok, what):
     if not ok:
         raise ValueError(what)
@@ -30,6 +38,31 @@ def _check_scales(scales, num_pages, page_size, num_kv_heads, scale_block, devic
     _require(scales.numel() == num_pages * page_size // scale_block * num_kv_heads,
              f"{name}: one scale for each block of {scale_block} tokens and kv head "
              f"([num_pages * page_size / scale_block, num_kv_heads])")
+
+
+def _attention_options(problem, device, k_pool, v_pool, k_scales, v_scales, scale_block,
+                       logit_cap, alibi_slopes):
+    """The run's ``pa_attention_options``, or None if nothing is asked for."""
+    if k_scales is None and v_scales is None and scale_block is None:
+        if alibi_slopes is None and not logit_cap:
+            return None
+        scale_block = 0
+    else:
+        _require(k_scales is not None and v_scales is not None, "k_scales and v_scales together")
+        if scale_block is None:
+            scale_block = problem.page_size
+        _require(scale_block > 0 and problem.page_size % scale_block == 0,
+                 "scale_block divides the page")
+        pages = k_pool.numel() // (problem.page_size * problem.num_kv_heads * problem.head_dim)
+        for name, scales in (("k_scales", k_scales), ("v_scales", v_scales)):
+            _check_scales(scales, pages, problem.page_size, problem.num_kv_heads, scale_block,
+                          device, name)
+    if alibi_slopes is not None:
+        _require(alibi_slopes.dtype == torch.float32 and alibi_slopes.device == device
+                 and alibi_slopes.is_contiguous() and alibi_slopes.numel() == problem.num_qo_heads,
+                 f"alibi_slopes: float32 on {device}, one per query head")
+    return C.make_options(k_scales=k_scales, v_scales=v_scales, scale_block=scale_block,
+                          logit_cap=logit_cap, alibi_slopes=alibi_slopes)
 
 
 class PagedDecode:
@@ -45,8 +78,8 @@ class PagedDecode:
                  ctas_per_sm=None, min_chunk_tokens=0, prefix_len=0, flags=0,
                  piece_cost_tokens=0, kv_dtype=None, k_scale=1.0, v_scale=1.0,
                  rope_theta=0.0, stream=None):
-        self.device = torch.device(device if device is not None else "cuda")
-        dev_index = self.device.index if self.device.index is not None else torch.cuda.current_device()
+        self.device = _device(device)
+        dev_index = self.device.index
         self.dtype = dtype
         self.batch = len(last_page_len)
         self.num_qo_heads, self.head_dim = num_qo_heads, head_dim
@@ -80,7 +113,17 @@ class PagedDecode:
         return C.pa_plan_work_items(self.plan)
 
     def run(self, q, k_pool, v_pool, kv_indices, o=None, lse=None, prefix_indices=None,
-            stream=None):
+            stream=None, *, k_scales=None, v_scales=None, scale_block=None, logit_cap=0.0,
+            alibi_slopes=None):
+        """``k_scales`` / ``v_scales`` (float32 ``[num_pages * page_size /
+        scale_block, num_kv_heads]``, 8-bit pools): a scale for each block of
+        ``scale_block`` tokens (default: a page) and kv head, as ``PagedKV``
+        writes them.  ``logit_cap``: scores become ``cap * tanh(s / cap)``;
+        ``alibi_slopes`` (float32 ``[num_qo_heads]``): scores lose slope *
+        distance.  None of them goes with a shared prefix."""
+        options = _attention_options(self.problem, self.device, k_pool, v_pool, k_scales,
+                                     v_scales, scale_block, logit_cap, alibi_slopes)
+        _require(options is None or not self.prefix_len, "a cascade run takes no options")
         if o is None:
             o = torch.empty(self.batch, self.num_qo_heads, self.head_dim,
                             dtype=_TORCH_DTYPES[self.dtype], device=self.device)
@@ -90,6 +133,10 @@ class PagedDecode:
         if self.prefix_len:
             C.pa_cascade_run(self.plan, q, k_pool, v_pool, prefix_indices, kv_indices, o, lse,
                              self.workspace, self.workspace.numel(), stream)
+        elif options is not None:
+            with torch.cuda.device(self.device):
+                C.pa_run_options(self.plan, options, q, k_pool, v_pool, kv_indices, o, lse,
+                                 self.workspace, self.workspace.numel(), stream)
         else:
             C.pa_run(self.plan, q, k_pool, v_pool, kv_indices, o, lse, self.workspace,
                      self.workspace.numel(), stream)
@@ -109,7 +156,7 @@ class PagedPrefill:
     def __init__(self, qo_indptr, kv_indptr, last_page_len, *, num_qo_heads, num_kv_heads,
                  page_size, dtype, sm_scale, num_pages, causal=True, head_dim=128, device=None,
                  num_sms=None, flags=0, stream=None):
-        self.device = torch.device(device if device is not None else "cuda")
+        self.device = _device(device)
         self.dtype = dtype
         self.batch = len(last_page_len)
         self.total_q = int(qo_indptr[-1]) if self.batch else 0
@@ -135,15 +182,25 @@ class PagedPrefill:
     def cta_indptr(self):
         return C.pa_plan_cta_indptr(self.plan)
 
-    def run(self, q, k_pool, v_pool, kv_indices, o=None, lse=None, stream=None):
+    def run(self, q, k_pool, v_pool, kv_indices, o=None, lse=None, stream=None, *, logit_cap=0.0,
+            alibi_slopes=None):
+        """``logit_cap`` and ``alibi_slopes`` as for ``PagedDecode.run``; slopes
+        need the causal mask."""
+        options = _attention_options(self.problem, self.device, k_pool, v_pool, None, None, None,
+                                     logit_cap, alibi_slopes)
         if o is None:
             o = torch.empty(self.total_q, self.num_qo_heads, self.head_dim,
                             dtype=_TORCH_DTYPES[self.dtype], device=self.device)
         if lse is None:
             lse = torch.empty(self.total_q, self.num_qo_heads, dtype=torch.float32,
                               device=self.device)
-        C.pa_prefill_run(self.plan, q, k_pool, v_pool, kv_indices, o, lse, self.workspace,
-                         self.workspace.numel(), stream)
+        if options is not None:
+            with torch.cuda.device(self.device):
+                C.pa_prefill_run_options(self.plan, options, q, k_pool, v_pool, kv_indices, o,
+                                         lse, self.workspace, self.workspace.numel(), stream)
+        else:
+            C.pa_prefill_run(self.plan, q, k_pool, v_pool, kv_indices, o, lse, self.workspace,
+                             self.workspace.numel(), stream)
         return o, lse
 
     def check(self, stream=None) -> int:
@@ -167,9 +224,7 @@ class PagedKV:
     def __init__(self, qo_indptr, kv_indptr, last_page_len, *, num_kv_heads, page_size, dtype,
                  kv_dtype, num_pages, scale_block=None, head_dim=128, device=None, flags=0,
                  stream=None):
-        self.device = torch.device(device if device is not None else "cuda")
-        if self.device.index is None:
-            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.device = _device(device)
         self.dtype, self.kv_dtype = dtype, kv_dtype
         self.batch = len(last_page_len)
         _require(len(qo_indptr) == self.batch + 1 and len(kv_indptr) == self.batch + 1,

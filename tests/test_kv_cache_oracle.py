@@ -229,3 +229,41 @@ def test_kv_run_argument_checks(C):
     idle = C.pa_kv_plan_create(_kv_problem(C), 16, [0, 0, 0], [0, 1, 3], [5, 4])
     C.pa_kv_append(idle, None, 0, None, 0, None, None, None, None, None, a,
                    C.pa_plan_workspace_bytes(idle), 0)
+
+
+def test_option_checks(C):
+    """Refused on the host, before anything is enqueued."""
+    w = W.make_workload("v", [20, 40], num_qo_heads=8, num_kv_heads=2, page_size=16, dtype="f16",
+                        seed=1, qo_lens=[4, 4])
+    a, big = 1 << 20, 1 << 30
+
+    def problem(**kw):
+        return C.make_problem(**{**dict(batch=2, num_qo_heads=8, num_kv_heads=2, page_size=16,
+                                        dtype="f16", sm_scale=0.1, num_sms=4, ctas_per_sm=1,
+                                        num_pages=w.num_pages), **kw})
+
+    def status(plan, run=None, **kw):
+        with pytest.raises(C.PagedAttnError) as e:
+            (run or C.pa_run_options)(plan, C.make_options(**kw), a, a, a, a, a, None, a, big, 0)
+        return e.value.status
+
+    tables = (w.kv_indptr, w.last_page_len)
+    p16, p8 = C.pa_plan_create(problem(), *tables), C.pa_plan_create(problem(kv_dtype="e4m3"), *tables)
+    scaled = dict(k_scales=a, v_scales=a, scale_block=16)
+    assert status(p16, **scaled) == C.PA_ERR_INVALID_ARG               # 16-bit pools
+    for kw in (dict(k_scales=None), dict(v_scales=None), dict(scale_block=0), dict(scale_block=-4),
+               dict(scale_block=3), dict(scale_block=32), dict(k_scales=a + 2)):
+        assert status(p8, **{**scaled, **kw}) == C.PA_ERR_INVALID_ARG, kw
+    other = C.pa_plan_create(problem(kv_dtype="e4m3", k_scale=0.5), *tables)
+    assert status(other, **scaled) == C.PA_ERR_INVALID_ARG             # two kinds of scales
+    for cap in (-1.0, float("nan"), float("inf"), 2.0 ** 21, 2.0 ** -21):
+        assert status(p16, logit_cap=cap) == C.PA_ERR_INVALID_ARG
+    assert status(p16, alibi_slopes=a + 1) == C.PA_ERR_INVALID_ARG
+    cascade = C.pa_cascade_plan_create(problem(), 32, *tables)
+    assert status(cascade, logit_cap=1.0) == C.PA_ERR_INVALID_ARG
+    pre = [C.pa_prefill_plan_create(problem(), causal, w.qo_indptr, *tables) for causal in (1, 0)]
+    assert status(pre[0], logit_cap=1.0) == C.PA_ERR_INVALID_ARG       # not a decode plan
+    assert status(p16, C.pa_prefill_run_options, logit_cap=1.0) == C.PA_ERR_INVALID_ARG
+    assert status(pre[0], C.pa_prefill_run_options, **scaled) == C.PA_ERR_UNSUPPORTED
+    assert status(pre[1], C.pa_prefill_run_options, alibi_slopes=a) == C.PA_ERR_UNSUPPORTED
+    assert status(pre[1], C.pa_prefill_run_options, logit_cap=-2.0) == C.PA_ERR_INVALID_ARG
