@@ -506,13 +506,13 @@ __device__ __forceinline__ void run_piece(const DecodeArgs& a, const pa_work_ite
   constexpr int kStages = C::kStages;
   const PieceCopier<C, kCheckMode, kScaled> cp(a, it, smem, scale_ring);
   if (!started) cp.start(pg);
-  // options: this lane's head's bias per unit of distance, the query's position
-  float slope2 = 0.f;
-  int qpos = 0;
+  // options: this lane's head's bias per unit of distance, and the distance
+  // to this thread's first token of the tile, less one tile per tile
+  float slope2 = 0.f, dist = 0.f;
   if constexpr (kExt) {
     if (a.score.slopes) {
       slope2 = __ldg(a.score.slopes + hq0 + my_head) * kLog2e;
-      qpos = __ldg(a.kv_len + b) - 1;
+      dist = float(__ldg(a.kv_len + b) - 1 - (tb + grp));
     }
   }
 
@@ -577,11 +577,12 @@ __device__ __forceinline__ void run_piece(const DecodeArgs& a, const pa_work_ite
       float r = reduce_scatter<G, LT>(part) * a.score_scale;
       if constexpr (kExt) {
         if constexpr (kScaled) r *= kscale[j];
-        const float dist = float(qpos - (tb + t * kTile + grp + kGroups * j));
-        r = final_score(r, a.score, slope2, dist);
+        r = final_score(r, a.score, slope2, dist - float(kGroups * j));
       }
       sc[j] = (t * kTile + grp + kGroups * j < len) ? r : -INFINITY;
     }
+
+    if constexpr (kExt) dist -= float(kTile);
 
     // Lazy running max: the reference point m moves only when a score beats
     // it by more than kSlack (base 2), so p = 2^(s - m) <= 2^kSlack and o is

@@ -1,8 +1,8 @@
 // Runs of the CUDA-core decode kernel with options (pa_run_options): capped
 // scores and distance bias over 16-bit pools, 8-bit pools with block scales,
 // and either with rotary positions.  The kernel template is decode_kernel.cuh
-// (kExt); this file only instantiates it.  The index check and every option
-// are launch arguments, which keeps the number of instantiations down.
+// (kExt); this file only instantiates it.  Which options apply is a launch
+// argument; so is the index check on the fp32 path, as without options.
 #include <cuda_runtime.h>
 
 #include "decode_kernel.cuh"
@@ -20,9 +20,12 @@ cudaError_t dispatch_rope(bool rope, int group, const dec::DecodeArgs& a, int64_
 template <typename Tag>
 cudaError_t dispatch_kv(pa_dtype kv, bool rope, int group, const dec::DecodeArgs& a, int64_t n,
                         cudaStream_t s) {
+  using dec::KV16;
   if (kv == PA_E4M3) return dispatch_rope<Tag, dec::E4M3>(rope, group, a, n, s);
   if (kv == PA_E5M2) return dispatch_rope<Tag, dec::E5M2>(rope, group, a, n, s);
-  return dispatch_rope<Tag, dec::KV16>(rope, group, a, n, s);
+  if (rope) return dec::dispatch_group<Tag, KV16, dec::kRuntimeCheck, true, true>(group, a, n, s);
+  return a.check ? dec::dispatch_group<Tag, KV16, dec::kChecked, false, true>(group, a, n, s)
+                 : dec::dispatch_group<Tag, KV16, dec::kNoCheck, false, true>(group, a, n, s);
 }
 
 }  // namespace

@@ -35,7 +35,8 @@ int decode_tc_ctas_per_sm(int32_t group, pa_dtype dtype, int32_t* out) {
                                        Off<false, false>::kSmemBytes);
   int n = 0;
   if (e == cudaSuccess)
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, Off<false, false>::kSmemBytes);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads,
+                                                      Off<false, false>::kSmemBytes);
   *out = n;
   return int(e);
 }

@@ -47,9 +47,15 @@
 // fp16 (exact: 4 significant bits each), P into 4 terms (16 significant
 // bits).  Term k of head h is column k * G + h of S^T (resp. O^T); the
 // softmax (resp. epilogue) adds the columns back with weights 16^-k.
-// Options (kExt; pa_run_options).  Block scales of an 8-bit pool ride with
-// their rows: each loader lane copies its token's K and V scale with 4-byte
-// cp.async into the stage, counted by the stage's barrier.  The K scale
+// Options (kExt; pa_run_options).  8-bit pools: the K and the V half of a ring
+// stage have barriers of their own (kSep).  K is free once S has been computed,
+// and V is asked for one tile after K, so a stage does not wait for the
+// softmax: with one barrier pair per stage the ring's own cycle (issue, load,
+// S, softmax, P V, refill) took 3,111 cycles a tile of the ragged batch where
+// HBM needs 2,800.  Block scales ride ahead of their K rows: each loader lane
+// copies its tokens' K and V scale with 4-byte cp.async into one of four slots
+// with a barrier each.  Slot t % 4 is refilled for tile t + 4 after V(t + 3),
+// so after P V(t), which the softmax's reading of tile t precedes.  The K scale
 // multiplies the token's scores; the V scale v enters through the weights,
 // w = 2^(s - m) v in P's place, with the lazy reference m kept on s + log2 v,
 // so w <= 2^8 keeps P's range whatever the scales; the row sum takes 2^(s - m),
@@ -112,6 +118,7 @@ template <> struct Lay<false> {
   static constexpr int kBarFull = kBarPath, kBarEmpty = kBarFull + kStages;
   static constexpr int kNumBars = kBarEmpty + kStages;
   static constexpr uint32_t kTmemCols = 64;         // S0, S1, O0, O1: 16 columns each
+  static constexpr int kScaleSlots = 0, kNumBarsOptions = kNumBars;
 };
 template <> struct Lay<true> {
   static constexpr int kStages = 3;
@@ -123,6 +130,11 @@ template <> struct Lay<true> {
   static constexpr int kNumBars = kBarEmpty + kStages;
   // S0, S1 (two 128-token halves each), O0, O1: up to 32 columns each
   static constexpr uint32_t kTmemCols = 256;
+  // with options: barriers of the V half of a stage, and the ring of scales
+  static constexpr int kScaleSlots = 4;
+  static constexpr int kBarVFull = kNumBars, kBarVEmpty = kBarVFull + kStages,
+                       kBarScales = kBarVEmpty + kStages;
+  static constexpr int kNumBarsOptions = kBarScales + kScaleSlots;
 };
 template <bool k8, bool kExt> struct Off {
   static constexpr int kOffQ = Lay<k8>::kOffQ;
@@ -133,10 +145,11 @@ template <bool k8, bool kExt> struct Off {
   static constexpr int kOffL = kOffX + 2 * 4 * kN * 4;  // row sums    [2][4 warps][16]
   static constexpr int kOffM = kOffL + 2 * 4 * kN * 4;  // a piece's final maxima [2][16]
   static constexpr int kOffQS = kOffM + 2 * kN * 4;     // 8-bit pools: score scale per head [2][16]
-  static constexpr int kOffS = kOffQS + 2 * kN * 4;  // 8-bit options: scales [stage][K, V][256]
+  static constexpr int kOffS = kOffQS + 2 * kN * 4;  // 8-bit options: scales [slot][K, V][256]
   static constexpr int kScaleBytes = 2 * 2 * kTok * 4;
-  static constexpr int kOffBar = kOffS + (k8 && kExt ? Lay<k8>::kStages * kScaleBytes : 0);
-  static constexpr int kSmemBytes = kOffBar + Lay<k8>::kNumBars * 8 + 16 + 1024;  // + alignment
+  static constexpr int kNumBars = kExt ? Lay<k8>::kNumBarsOptions : Lay<k8>::kNumBars;
+  static constexpr int kOffBar = kOffS + (kExt ? Lay<k8>::kScaleSlots : 0) * kScaleBytes;
+  static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16 + 1024;  // + alignment
   static_assert(kSmemBytes <= 232448, "shared memory");
   static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0,
                 "128-byte swizzle atoms need 1 KB alignment");
@@ -171,7 +184,6 @@ struct TcArgs {
   const float* v_scales;
   const int32_t* kv_len;
   int32_t log2_block;
-  bool check;
   ScoreArgs score;
 };
 
@@ -296,18 +308,19 @@ __device__ __forceinline__ __half2 e4m3x2_value(uint16_t c) {
   return *reinterpret_cast<__half2*>(&d);
 }
 
-// Two P values (in [0, 2^8]) as four E4M3 terms p ~ t0 + t1/16 + t2/256 +
-// t3/4096: t0 = e4m3(p); the residual (p - t0) * 16 is exact in fp32 and
-// rounded to fp16 (11 more bits, ~15 in all); t1..t3 take it apart exactly.
-__device__ __forceinline__ void split_p4(float lo, float hi, uint16_t (&t)[4]) {
+// Two P values (below 448) as n E4M3 terms p ~ t0 + t1/16 + t2/256 (+
+// t3/4096): t0 = e4m3(p); the residual (p - t0) * 16 is exact in fp32 and
+// rounded to fp16 (11 more bits, ~15 in all); t1.. take it apart, exactly for n = 4.
+template <int n>
+__device__ __forceinline__ void split_p(float lo, float hi, uint16_t (&t)[n]) {
   t[0] = e4m3x2(lo, hi);
   const float2 v = __half22float2(e4m3x2_value(t[0]));
   __half2 r = __floats2half2_rn((lo - v.x) * 16.f, (hi - v.y) * 16.f);
   const __half2 k16 = __float2half2_rn(16.f);
 #pragma unroll
-  for (int k = 1; k < 4; ++k) {
+  for (int k = 1; k < n; ++k) {
     t[k] = e4m3x2(r);
-    if (k < 3) r = __hmul2(__hsub2(r, e4m3x2_value(t[k])), k16);
+    if (k < n - 1) r = __hmul2(__hsub2(r, e4m3x2_value(t[k])), k16);
   }
 }
 
@@ -353,16 +366,17 @@ __device__ __forceinline__ int next_nonempty(const pa_work_item* items, int pc, 
   return pc;
 }
 
-// Plain runs (index check off or on), or a run with options (kExt: the check
-// and every option are launch arguments, which keeps the instantiations down).
-enum TcMode { kTcPlain = 0, kTcChecked = 1, kTcOptions = 2 };
+// Plain runs and runs with options (kExt: which ones are launch arguments), the
+// index check off or on.  The check is compiled in or out: as a launch argument
+// its test waited for every page index where it was loaded (1,550 cycles a tile).
+enum TcMode { kTcPlain = 0, kTcChecked = 1, kTcOptions = 2, kTcOptionsChecked = 3 };
 
 // 8-bit pools: the code type (1 = E4M3, 2 = E5M2), 0 for 16-bit pools.
 template <typename Tag, int KV8, int G, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcArgs a) {
   constexpr bool k8 = KV8 != 0;
-  constexpr bool kExt = kMode == kTcOptions;
-  const bool check = kExt ? a.check : kMode == kTcChecked;
+  constexpr bool kExt = kMode >= kTcOptions;
+  constexpr bool kCheck = kMode == kTcChecked || kMode == kTcOptionsChecked;
   // 16-bit pools, two-term P: P^T rows [0, G) hold hi = round(p), rows
   // [G, 2G) lo = round(p - hi); O^T columns likewise, added in the epilogue.
   // Needed for bf16 P (8 bits).  With options fp16 P takes it too (it costs
@@ -370,13 +384,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
   // rounding of P, and a lone 11-bit P would leave o up to 2^-11 |v| off them.
   constexpr bool kSplit = !k8 && (Fmt<Tag>::v == 1 || kExt);
   // 8-bit pools: E4M3 terms of q (kQT) and of P (kPT) per head.
-  constexpr int kQT = Fmt<Tag>::v == 1 ? 2 : 3, kPT = 4;
+  // With options a softmax thread has more to do per score, and P takes three:
+  // 12 significant bits (an fp16 P's 11 and one more).  The reference is set
+  // 2^kHead below the maximum, so that the smallest step, 2^-17 of the reference,
+  // is 2^-21 of the largest weight as with four terms (many tokens far below it,
+  // as behind an attention sink, still count), and moves when a weight would
+  // pass 2^8.7 (E4M3 holds 448).  A larger kHead would move it too often: with
+  // 7, a factor of 2 over the first maximum is enough, and each move waits for
+  // the P V in flight (tile period 4,460 cycles for 3,165 at group 8).
+  constexpr int kQT = Fmt<Tag>::v == 1 ? 2 : 3, kPT = kExt ? 3 : 4;
+  constexpr float kHead = k8 && kExt ? 4.f : 0.f;
+  constexpr float kMove = k8 && kExt ? 8.7f : kSlack;
   // columns of one S^T / O^T buffer (the MMA N)
   constexpr int kNC = k8 ? (kPT * G <= 16 ? 16 : 32) : kN;
   // S^T columns a softmax thread reads, O^T columns the epilogue reads
   constexpr int kSC = k8 ? pow2_at_least(kQT * G) : G;
   constexpr int kCols = k8 ? kPT * G : (kSplit ? 2 * G : G);
-  static_assert(kCols <= kNC && kSC <= kNC, "terms must fit the MMA N");
+  constexpr int kColsLd = pow2_at_least(kCols);  // as loaded and stored
+  static_assert(kColsLd <= kNC && kSC <= kNC, "terms must fit the MMA N");
   // tokens per tile: 128-token halves, each one S^T MMA (M = 128, a TMEM lane
   // per token) and each handled by the same softmax thread
   constexpr int kHalves = k8 ? 2 : 1, kTT = kHalves * kTok;
@@ -386,7 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
   using O = Off<k8, kExt>;
   constexpr int kOffQ = O::kOffQ, kOffP = O::kOffP, kOffX = O::kOffX, kOffL = O::kOffL,
                 kOffM = O::kOffM, kOffQS = O::kOffQS, kOffBar = O::kOffBar;
-  constexpr int kNumBars = L::kNumBars;
+  constexpr int kNumBars = O::kNumBars;
+  constexpr bool kSep = k8 && kExt;  // K and V of a stage come and go on their own
   constexpr uint32_t kTmemCols = L::kTmemCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -402,7 +428,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(bar(L::kBarFull + s), 128);
       mbar_init(bar(L::kBarEmpty + s), 1);
+      if constexpr (kSep) {
+        mbar_init(bar(L::kBarVFull + s), 128);
+        mbar_init(bar(L::kBarVEmpty + s), 1);
+      }
     }
+    if constexpr (kSep)
+      for (int s = 0; s < L::kScaleSlots; ++s) mbar_init(bar(L::kBarScales + s), 128);
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar(kBarS + b), 1);
       mbar_init(bar(kBarSFree + b), 4);
@@ -450,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
       if (mypos >= wlen) return -1;
       const int idx = (w.token_begin + mypos) >> lp;
       int pg = __ldg(a.kv_indices + w.page_begin + idx);
-      if (check && (pg < 0 || int64_t(pg) >= a.num_pages)) {
+      if (kCheck && (pg < 0 || int64_t(pg) >= a.num_pages)) {
         atomicMin(a.error_pos, (unsigned long long)(w.page_begin + idx));
         pg = -1;
       }
@@ -486,9 +518,113 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
       }
       return r;
     };
+    bool ok = true;
+    if constexpr (kSep) {
+      // Per step V of tile t, then the scales and K of tile t + 1 (see kSep at
+      // the top).  The K walker is one tile ahead of the V walker, the page
+      // lookups three ahead of K.
+      struct Walk {
+        int pi, tt, len;
+        pa_work_item it;
+      };
+      Walk wk{pi, 0, len, it}, wv = wk;
+      auto advance = [&](Walk& w) {
+        if (++w.tt * kTT < w.len) return;
+        w.tt = 0;
+        w.pi = next_nonempty(a.items, w.pi + 1, p1);
+        if (w.pi < p1) {
+          w.it = a.items[w.pi];
+          w.len = w.it.token_end - w.it.token_begin;
+        }
+      };
+      auto row_of = [&](const Walk& w, int page, int r) -> uint32_t {
+        const uint32_t pos = uint32_t(w.it.token_begin + w.tt * kTT + r);
+        return page >= 0 ? ((uint32_t(page) << lp) | (pos & pmask)) : 0u;
+      };
+      // Lookups, addresses and copies each in a loop of their own: the copies
+      // are volatile and keep their order, so one loop would take a shuffle's
+      // and an address's latency per copy (3,500 cycles a tile; HBM needs 2,800).
+      auto copy = [&](const Walk& w, const Pg& pg, const uint8_t* pool, uint32_t dst, int full) {
+        const uint64_t base =
+            reinterpret_cast<uint64_t>(pool + int64_t(w.it.kv_head) * kRowBytes) + c * 16;
+        constexpr int kSteps = 32 / kRowsPer;
+        int page[kHalves][kSteps];
+        uint64_t from[kHalves][kSteps];
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k)
+            page[h][k] = __shfl_sync(0xffffffffu, pg.v[h], kRowsPer * k + lane / kLanesRow);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k)
+            from[h][k] = base + uint64_t(row_of(w, page[h][k], kTok * h + 32 * lw + kRowsPer * k +
+                                                                    lane / kLanesRow)) *
+                                    pool_row_bytes;
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            const int r = kTok * h + 32 * lw + kRowsPer * k + lane / kLanesRow;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                             dst + sw_chunk(r, c, kHalfKV)),
+                         "l"(from[h][k]), "r"(page[h][k] >= 0 ? 16u : 0u)
+                         : "memory");
+          }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar(full))
+                     : "memory");
+      };
+      auto load_k = [&](int t, const Pg& pg) {  // scales and K of tile t
+        if (a.k_scales) {
+          const int slot = t % L::kScaleSlots;
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) {
+            const int r = kTok * h + 32 * lw + lane;
+            const uint32_t row = row_of(wk, pg.v[h], r);
+            const uint32_t nbytes = pg.v[h] >= 0 ? 4u : 0u;
+            const int64_t at = int64_t(row >> a.log2_block) * a.num_kv_heads + wk.it.kv_head;
+            const uint32_t dst = sb + O::kOffS + slot * O::kScaleBytes + r * 4;
+            cp_async4(dst, a.k_scales + at, nbytes);
+            cp_async4(dst + kTT * 4, a.v_scales + at, nbytes);
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(
+                           bar(L::kBarScales + slot))
+                       : "memory");
+        }
+        copy(wk, pg, a.k_pool, sb + L::kOffRing + (t % kStages) * kStageBytes,
+             L::kBarFull + t % kStages);
+        advance(wk);
+      };
+      Pg pg0 = look(), pg1 = look(), pg2 = look(), pg3 = look();
+      int t = 0;
+      if (wk.pi < p1) load_k(0, pg0);
+      auto step = [&](Pg& pv, const Pg& pk) -> bool {
+        if (wv.pi >= p1) return false;
+        if (t >= kStages) {  // P V(t - 3) done: its V stage and tile t - 3's scales are free
+          ok = mbar_wait(bar(L::kBarVEmpty + t % kStages), ((t / kStages) - 1) & 1);
+          if (!ok) return false;
+        }
+        copy(wv, pv, a.v_pool, sb + L::kOffRing + (t % kStages) * kStageBytes + kVOff,
+             L::kBarVFull + t % kStages);
+        advance(wv);
+        pv = look();
+        if (wk.pi < p1) {
+          const int n = t + 1;
+          if (n >= kStages) {  // S(n - 3) done
+            ok = mbar_wait(bar(L::kBarEmpty + n % kStages), ((n / kStages) - 1) & 1);
+            if (!ok) return false;
+          }
+          load_k(n, pk);
+        }
+        ++t;
+        return true;
+      };
+      while (step(pg0, pg1) && step(pg1, pg2) && step(pg2, pg3) && step(pg3, pg0)) {
+      }
+    } else {
     Pg pg0 = look(), pg1 = look(), pg2 = look();
     int t = 0;
-    bool ok = true;
     // copies tile t with the page indices in pg, then reloads pg three tiles on
     auto step = [&](Pg& pg) -> bool {
       if (pi >= p1) return false;
@@ -526,21 +662,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
                        : "memory");
         }
       }
-      if constexpr (k8 && kExt) {
-        if (a.k_scales) {  // this lane's rows' scales
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h) {
-            const int r = kTok * h + 32 * lw + lane;
-            const uint32_t pos = uint32_t(it.token_begin + tt * kTT + r);
-            const bool in = pg.v[h] >= 0;
-            const uint32_t row = in ? ((uint32_t(pg.v[h]) << lp) | (pos & pmask)) : 0u;
-            const int64_t at = int64_t(row >> a.log2_block) * a.num_kv_heads + it.kv_head;
-            const uint32_t dst = sb + O::kOffS + s * O::kScaleBytes + r * 4;
-            cp_async4(dst, a.k_scales + at, in ? 4u : 0u);
-            cp_async4(dst + kTT * 4, a.v_scales + at, in ? 4u : 0u);
-          }
-        }
-      }
       // the stage's barrier counts this thread once all its copies above land
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(
                        bar(L::kBarFull + s))
@@ -558,6 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
       return true;
     };
     while (step(pg0) && step(pg1) && step(pg2)) {
+    }
     }
     if (!ok) {
       asm volatile("cp.async.wait_all;\n" ::: "memory");
@@ -601,6 +723,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
         auto k_ready = [&]() {
           return test(L::kBarFull + ts % kStages, (ts / kStages) & 1);
         };
+        auto v_ready = [&]() {  // with K, unless they come on their own
+          if constexpr (kSep) return test(L::kBarVFull + tv % kStages, (tv / kStages) & 1);
+          return true;
+        };
         if (s_piece < p1 &&
             (ts < 2 || test(kBarSFree + (ts & 1), ((ts - 2) >> 1) & 1)) &&
             k_ready() && test(kBarQReady + (s_np & 1), (s_np >> 1) & 1)) {
@@ -629,6 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
               }
             }
             tc::commit(bar(kBarS + (ts & 1)));
+            if constexpr (kSep) tc::commit(bar(L::kBarEmpty + ts % kStages));  // K is read
           }
           __syncwarp();
           ++ts;
@@ -640,8 +767,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
           }
           progress = true;
         }
-        if (tv < ts && test(kBarPReady + (tv & 1), (tv >> 1) & 1) &&
+        if (tv < ts && test(kBarPReady + (tv & 1), (tv >> 1) & 1) && v_ready() &&
             (v_tile > 0 || v_np < 2 || test(kBarOFree + (v_np & 1), ((v_np - 2) >> 1) & 1))) {
+          if constexpr (kSep) fence_proxy_async_smem();  // V's copies, as above for K
           tc::fence_after_sync();
           const uint64_t vd = dv0 + uint64_t(((tv % kStages) * kStageBytes) >> 4);
           const uint64_t pd = dp0 + uint64_t(((tv & 1) * kPB) >> 4);
@@ -666,7 +794,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
               }
             }
             tc::commit(bar(kBarPFree + (tv & 1)));
-            tc::commit(bar(L::kBarEmpty + tv % kStages));
+            if constexpr (kSep) tc::commit(bar(L::kBarVEmpty + tv % kStages));
+            else tc::commit(bar(L::kBarEmpty + tv % kStages));
             if (last) tc::commit(bar(kBarODone + (v_np & 1)));
           }
           __syncwarp();
@@ -758,30 +887,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
         // the V scale `vs`, by which a token's weight in P V exceeds its p
         float vs[kHalves], lv[kHalves];
         if constexpr (kExt) {
-          const bool scaled = k8 && a.k_scales;
-          if (scaled) {
-            // the tile's copies have landed (S was computed from them); waiting
-            // on their barrier makes the scales visible to this thread
-            ok = __all_sync(0xffffffffu,
-                            mbar_wait(bar(L::kBarFull + t % L::kStages), (t / L::kStages) & 1));
-            if (!ok) break;
+          float kscale[kHalves];
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) {
+            kscale[h] = 1.f;
+            vs[h] = 1.f;
+            lv[h] = 0.f;
+          }
+          if constexpr (kSep) {
+            if (a.k_scales) {
+              const int slot = t % L::kScaleSlots;
+              ok = __all_sync(0xffffffffu,
+                              mbar_wait(bar(L::kBarScales + slot), (t / L::kScaleSlots) & 1));
+              if (!ok) break;
+              const float* sc = reinterpret_cast<const float*>(smem + O::kOffS + slot * O::kScaleBytes);
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h) {
+                kscale[h] = sc[kTok * h + i];
+                vs[h] = sc[kTT + kTok * h + i];
+                lv[h] = fmaxf(fast_log2(fabsf(vs[h])), -60.f);  // a zero scale's -inf, too
+              }
+            }
           }
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
-            float kscale = 1.f;
-            vs[h] = 1.f;
-            lv[h] = 0.f;
-            if (scaled) {
-              const float* sc = reinterpret_cast<const float*>(smem + O::kOffS +
-                                                               (t % L::kStages) * O::kScaleBytes);
-              kscale = sc[kTok * h + i];
-              vs[h] = sc[kTT + kTok * h + i];
-              lv[h] = fmaxf(fast_log2(fabsf(vs[h])), -60.f);  // a zero scale's -inf, too
-            }
             const float dist = qpos - float(it.token_begin + tt * kTT + kTok * h + i);
 #pragma unroll
             for (int hh = 0; hh < G; ++hh)
-              sv[h][hh] = final_score(sv[h][hh] * kscale * scl[hh], a.score, slope2[hh], dist);
+              sv[h][hh] = final_score(sv[h][hh] * kscale[h] * scl[hh], a.score, slope2[hh], dist);
           }
         }
         // tile maximum per head over the tile's tokens: shuffles, then the 4 warps
@@ -803,14 +936,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
         float alpha[G], mn[G];
 #pragma unroll
         for (int hh = 0; hh < G; ++hh) {
-          const float tmax =
-              fmaxf(fmaxf(xm[hh], xm[kN + hh]), fmaxf(xm[2 * kN + hh], xm[3 * kN + hh])) *
-              (kExt ? 1.f : scl[hh]);
+          float tmax = fmaxf(fmaxf(xm[hh], xm[kN + hh]), fmaxf(xm[2 * kN + hh], xm[3 * kN + hh]));
+          if constexpr (!kExt) tmax *= scl[hh];
           alpha[hh] = 1.f;
           mn[hh] = m[hh];
-          if (tmax > m[hh] + kSlack) {
-            mn[hh] = tmax;
-            alpha[hh] = fast_exp2(m[hh] - tmax);  // m = -inf -> 0
+          if (tmax > m[hh] + kMove) {
+            mn[hh] = tmax - kHead;
+            alpha[hh] = fast_exp2(m[hh] - mn[hh]);  // m = -inf -> 0
             moved = true;
           }
         }
@@ -822,13 +954,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
           if (!ok) break;
           tc::fence_after_sync();
           const uint32_t oaddr = lane_addr + kColO + (np & 1) * kNC;
-          uint32_t r[kCols];
-          tmem_ld<kCols>(oaddr, r);
+          uint32_t r[kColsLd];
+          tmem_ld<kColsLd>(oaddr, r);
           tc::tmem_wait_ld();
 #pragma unroll
           for (int cc = 0; cc < kCols; ++cc)
             r[cc] = __float_as_uint(__uint_as_float(r[cc]) * alpha[cc % G]);
-          tmem_st<kCols>(oaddr, r);
+          tmem_st<kColsLd>(oaddr, r);
           tc::tmem_wait_st();
         }
         // P^T(t) for this thread's token; the row sums add the rounded values
@@ -861,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
 #pragma unroll
             for (int hh = 0; hh < G; hh += 2) {
               uint16_t tm[kPT];
-              split_p4(p[h][hh], hh + 1 < G ? p[h][hh + 1] : 0.f, tm);
+              split_p<kPT>(p[h][hh], hh + 1 < G ? p[h][hh + 1] : 0.f, tm);
 #pragma unroll
               for (int k = 0; k < kPT; ++k) {
                 const int n = k * G + hh;
@@ -918,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
       ++np;
     }
     if (!ok && lane == 0) flag_timeout(a);
-  } else if (warp >= 9) {
+  } else {
     // ------------------------------- epilogue -------------------------------
     // Warp 9 + j reads TMEM lanes 32 (warp % 4) .. + 31: head elements d.
     const int quarter = warp & 3;
@@ -1045,8 +1177,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
         ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarODone + (np & 1)), (np >> 1) & 1));
         if (!ok) break;
         tc::fence_after_sync();
-        uint32_t r[kCols];
-        tmem_ld<kCols>(lane_addr + kColO + (np & 1) * kNC, r);
+        uint32_t r[kColsLd];
+        tmem_ld<kColsLd>(lane_addr + kColO + (np & 1) * kNC, r);
         tc::tmem_wait_ld();
         tc::fence_before_sync();
         __syncwarp();
@@ -1140,7 +1272,8 @@ cudaError_t launch_tc_t(const TcArgs& a, int64_t n_cta, cudaStream_t stream) {
   // a cascade's decode level starts while the prefix level finishes
   const bool pdl = a.prefix_chunks > 0;
   auto kern = paged_decode_tc_kernel<Tag, KV8, G, kMode>;
-  constexpr int kSmem = Off<KV8 != 0, kMode == kTcOptions>::kSmemBytes;
+  constexpr bool kExt = kMode >= kTcOptions;
+  constexpr int kSmem = Off<KV8 != 0, kExt>::kSmemBytes;
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1152,7 +1285,8 @@ cudaError_t launch_tc_t(const TcArgs& a, int64_t n_cta, cudaStream_t stream) {
     configured.fetch_or(bit);
   }
   if (n_cta <= 0) return cudaSuccess;
-  return launch_maybe_dependent(kern, dim3(unsigned(n_cta)), dim3(kThreads), kSmem, stream, pdl, a);
+  return launch_maybe_dependent(kern, dim3(unsigned(n_cta)), dim3(kThreads), kSmem,
+                                stream, pdl, a);
 }
 
 template <typename Tag, int KV8, int kMode>

@@ -57,11 +57,22 @@
 // epilogue reads O.  Each half stages
 // its o rows in a 16 KB region of its own, 64 columns at a time.
 // Options (kExt; pa_prefill_run_options): the softmax warps turn the raw scores
-// into final base-2 scores as they are read.  A cap costs a polynomial of
-// tanh on the FMA pipe (score.cuh) while every |s| of a warp's tile is below
-// the cap, two MUFU operations per score in the rare tile where one is not;
-// the distance bias one FMA and one addition.  With a bias the tile maximum is
-// taken before the exponentials: the bias makes it grow from tile to tile.
+// into final base-2 scores relative to the row's reference as they are read,
+// so that the exponentials need no further operation.  The kernel is then
+// bound by the FMA pipe (a packed FMA takes two of its cycles), so operations
+// per score are what counts: the bias is one FMA; a cap is cap * tanh as x
+// times a polynomial in x^2 with every factor folded into its coefficients
+// (6 operations, bias added by the last) while the warp's scores are below half
+// the cap, a longer polynomial up to the cap, two MUFU operations per score in
+// the rare tile beyond; and all exponentials stay on the MUFU unit.  With a
+// distance bias the key tiles run last to first: the bias falls away from the
+// diagonal, so the first tile sets the reference and O is hardly ever rescaled
+// (in ascending order the maximum grows from tile to tile), and the
+// exponentials can be taken before the tile maximum is known, as without
+// options.  (Without a bias ascending order is the better one: its first tile
+// shows every row 128 keys, the diagonal tile as few as one.)  A half whose
+// rows see no key of the last tile then runs it fully masked, which keeps the
+// two halves' tiles aligned.
 // Every mbarrier wait is bounded; on a timeout the kernel records it in the
 // workspace status word and unwinds instead of hanging.  Every parity wait
 // targets a barrier whose previous phase the waiting thread has itself
@@ -140,6 +151,7 @@ struct PrefillArgs {
   float score_scale;                // sm_scale * log2(e), or as ScoreArgs has it
   int32_t check;                    // options: bounds-check page indices
   ScoreArgs score;                  // options
+  CapPoly cap;                      // options: the cap's polynomial in raw scores
 };
 
 // Plain runs (index check off or on), or a run with options (the check is a
@@ -178,7 +190,8 @@ struct Item {
   int h, q_begin, n_q, page_begin, kv_base, kv_end, nq0, nq1, nt0, nt1, ntiles;
 };
 
-__device__ __forceinline__ Item load_item(const PrefillArgs& a, int j) {
+// Last to first (rev), both halves run all of the item's tiles.
+__device__ __forceinline__ Item load_item(const PrefillArgs& a, int j, bool rev) {
   Item it;
   const int w = __ldg(a.sched + j);
   it.h = w % a.num_kv_heads;
@@ -194,7 +207,60 @@ __device__ __forceinline__ Item load_item(const PrefillArgs& a, int j) {
   it.nt0 = (min(it.kv_base + it.nq0, it.kv_end) + kKeys - 1) / kKeys;
   it.nt1 = it.nq1 > 0 ? (it.kv_end + kKeys - 1) / kKeys : 0;
   it.ntiles = max(it.nt0, it.nt1);
+  if (rev && it.nq1 > 0) it.nt0 = it.ntiles;
   return it;
+}
+
+// Final base-2 scores of a run with options, from raw ones: cap, then slope2 *
+// column (kBias), then base.
+template <bool kBias>
+struct OptionScores {
+  float2 s2, b2;
+  __device__ __forceinline__ OptionScores(float slope2, float base)
+      : s2(make_float2(slope2, slope2)), b2(make_float2(base, base)) {}
+  __device__ __forceinline__ float2 bias(int c) const {
+    return kBias ? __ffma2_rn(s2, make_float2(float(c), float(c + 1)), b2) : b2;
+  }
+  __device__ __forceinline__ float2 uncapped(const PrefillArgs& a, int c, float2 v) const {
+    return __ffma2_rn(v, make_float2(a.score_scale, a.score_scale), bias(c));
+  }
+  __device__ __forceinline__ float2 small(const CapPoly& cap, int c, float2 v) const {
+    const float2 u = __fmul2_rn(v, v);
+    float2 p = make_float2(cap.k[4], cap.k[4]);
+#pragma unroll
+    for (int i = 3; i >= 0; --i) p = __ffma2_rn(p, u, make_float2(cap.k[i], cap.k[i]));
+    return __ffma2_rn(v, p, bias(c));
+  }
+  // any |v|; which branch a tile takes is uniform in the warp
+  __device__ __forceinline__ void large(const PrefillArgs& a, float (&x)[kKeys], bool mid) const {
+    const float2 sc2 = make_float2(a.score_scale, a.score_scale);
+    const float2 cap2 = make_float2(a.score.cap_out, a.score.cap_out);
+    if (mid) {
+#pragma unroll
+      for (int c = 0; c < kKeys; c += 2)
+        put(x, c, __ffma2_rn(cap2, tanh_poly2(__fmul2_rn(make_float2(x[c], x[c + 1]), sc2)), bias(c)));
+    } else {
+#pragma unroll
+      for (int c = 0; c < kKeys; c += 2) {
+        const float2 y = __fmul2_rn(make_float2(x[c], x[c + 1]), sc2);
+        put(x, c, __ffma2_rn(cap2, make_float2(tanh_score(y.x), tanh_score(y.y)), bias(c)));
+      }
+    }
+  }
+  static __device__ __forceinline__ void put(float (&x)[kKeys], int c, float2 y) {
+    x[c] = y.x;
+    x[c + 1] = y.y;
+  }
+};
+
+// The largest |x| of a row.
+__device__ __forceinline__ float largest(const float (&x)[kKeys]) {
+  float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < kKeys; c += 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = max3(t[i], fabsf(x[c + 2 * i]), fabsf(x[c + 2 * i + 1]));
+  return max3(t[0], t[1], fmaxf(t[2], t[3]));
 }
 
 template <typename Tag, int kMode>
@@ -205,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kSplit = std::is_same<Tag, BF16>::value;
   constexpr bool kExt = kMode == kOptions;
   const bool check = kExt ? a.check != 0 : kMode == kChecked;
+  const bool rev = kExt && a.score.slopes;  // key tiles last to first
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -261,9 +328,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int j = j0; ok && j < j1; ++j) {
       const int jj = j - j0;
-      const Item it = load_item(a, j);
+      const Item it = load_item(a, j, rev);
       auto row_of = [&](int kt) -> int {
-        const int key = kt * kKeys + lane * box;
+        const int key = (rev ? it.ntiles - 1 - kt : kt) * kKeys + lane * box;
         if (lane >= nbox || kt >= it.ntiles) return 0;
         if (key >= it.kv_end) return a.oob_row;
         const int pos = it.page_begin + (key >> a.log2_page);
@@ -368,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int j = j0; ok && j < j1; ++j) {
         const int jj = j - j0;
-        const Item it = load_item(a, j);
+        const Item it = load_item(a, j, rev);
         const int nt[2] = {it.nt0, it.nt1};
         const int ntiles = it.ntiles;
         // Rows [zero_from, zero_to) of the last tile were copied from the page
@@ -388,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int g = vg + v;
               if (hf == 0 || v >= nt[0]) {  // the first half to use V(v) waits for it
                 ok = wait_all(kBarVFull + g % kVStages, (g / kVStages) & 1);
-                if (ok && v == ntiles - 1 && zero_from < zero_to) {
+                if (ok && v == (rev ? 0 : ntiles - 1) && zero_from < zero_to) {
                   uint8_t* vt = smem + kOffV + (g % kVStages) * kKVBytes;
                   const int n16 = (zero_to - zero_from) * 16;  // 16-byte chunks: 8 per row and half
                   for (int c = lane; c < n16; c += 32) {
@@ -459,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float slope2 = 0.f;  // options: bias per unit of distance, the row's position
       int qpos = 0;
       {
-        const Item it = load_item(a, j);
+        const Item it = load_item(a, j, rev);
         nt = hf ? it.nt1 : it.nt0;
         // keys this row may see (rows past the tile's tokens: all of the tile's
         // keys), and the fewest any row of the half sees
@@ -489,68 +556,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Keys at or past a row's limit are masked (a select: the score of a
         // stale row may be anything); tiles wholly below every row's limit need
         // no mask (uniform branch).
-        const int key0 = kt * kKeys;
-        if constexpr (kExt) {
-          const float2 sc2 = make_float2(a.score_scale, a.score_scale);
-          if (a.score.cap_out > 0.f) {
-            // scores as fractions of the cap, then cap_out * tanh
-            float umax = 0.f;
-#pragma unroll
-            for (int c = 0; c < kKeys; c += 2) {
-              const float2 y = __fmul2_rn(make_float2(x[c], x[c + 1]), sc2);
-              x[c] = y.x;
-              x[c + 1] = y.y;
-              umax = max3(umax, fabsf(y.x), fabsf(y.y));
-            }
-            if (__any_sync(0xffffffffu, !(umax <= 1.f))) {
-#pragma unroll
-              for (int c = 0; c < kKeys; ++c) x[c] = a.score.cap_out * tanh_score(x[c]);
-            } else {
-#pragma unroll
-              for (int c = 0; c < kKeys; c += 2) {
-                const float2 t = tanh_poly2(make_float2(x[c], x[c + 1]));
-                x[c] = a.score.cap_out * t.x;
-                x[c + 1] = a.score.cap_out * t.y;
-              }
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < kKeys; c += 2) {
-              const float2 y = __fmul2_rn(make_float2(x[c], x[c + 1]), sc2);
-              x[c] = y.x;
-              x[c + 1] = y.y;
-            }
-          }
-          if (a.score.slopes) {
-            // -slope2 * (qpos - (key0 + c)), the distance of key0 first
-            const float b0 = -slope2 * float(qpos - key0);
-            const float2 s2 = make_float2(slope2, slope2), b2 = make_float2(b0, b0);
-#pragma unroll
-            for (int c = 0; c < kKeys; c += 2) {
-              const float2 y = __fadd2_rn(make_float2(x[c], x[c + 1]),
-                                          __ffma2_rn(s2, make_float2(float(c), float(c + 1)), b2));
-              x[c] = y.x;
-              x[c + 1] = y.y;
-            }
-          }
-        }
+        const int key0 = (rev ? nt - 1 - kt : kt) * kKeys;
         const bool masked = key0 + kKeys > lim_min;
-        if (masked) {
+        auto mask = [&]() {
 #pragma unroll
           for (int c = 0; c < kKeys; ++c) x[c] = key0 + c < lim ? x[c] : -INFINITY;
-        }
-        auto write_p = [&](float mref, bool poly) -> float {
-          const float2 sc2 = make_float2(a.score_scale, a.score_scale);
-          const float2 nm2 = make_float2(-mref, -mref);
+        };
+        if (!kExt && masked) mask();
+        // P = 2^(score - ref) in the input type, 32 keys at a time: `score(c)` gives
+        // the pair of scores at column c and may put them into x on the way
+        auto write_p = [&](bool poly, auto&& score) -> float {
           float2 ps2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int c16 = 0; c16 < kKeys / 32; ++c16) {
             uint32_t w[16], wl[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int c = 32 * c16 + 2 * e;
-              const float2 a2 = kExt ? __fadd2_rn(make_float2(x[c], x[c + 1]), nm2)
-                                     : __ffma2_rn(make_float2(x[c], x[c + 1]), sc2, nm2);
+              const float2 a2 = score(32 * c16 + 2 * e);
               float2 p2;
               if (poly && (e & 7) < kPolyPairsPer8) {  // on the FMA pipe
                 p2 = exp2_poly2<kSplit ? 4 : 3>(a2);
@@ -574,6 +596,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 t = __fadd2_rn(ps2[0], ps2[1]);
           return t.x + t.y;
         };
+        auto raw = [&](int c) { return make_float2(x[c], x[c + 1]); };
+        auto scaled = [&](float ref) {
+          return [&, sc2 = make_float2(a.score_scale, a.score_scale),
+                  nm2 = make_float2(-ref, -ref)](int c) { return __ffma2_rn(raw(c), sc2, nm2); };
+        };
         auto tile_max = [&]() {
           float t0 = fmaxf(x[0], x[4]), t1 = fmaxf(x[1], x[5]), t2 = fmaxf(x[2], x[6]),
                 t3 = fmaxf(x[3], x[7]);
@@ -587,43 +614,92 @@ __global__ void __launch_bounds__(kThreads, 1)
           return max3(t0, t1, fmaxf(t2, t3)) * (kExt ? 1.f : a.score_scale);
         };
         float psum, alpha = 1.f;
-        if (kt == 0 || masked || (kExt && a.score.slopes)) {
+        auto rescale_o = [&](float factor) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float ov[32];
+            tc::tmem_ld32(lane_addr + col_o + 32 * c, ov);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] *= factor;
+            tc::tmem_st32(lane_addr + col_o + 32 * c, ov);
+          }
+        };
+        if constexpr (kExt) {
+          // x becomes the final score relative to the row's reference.  A row
+          // without one yet (it saw no key so far) takes its first tile's maximum;
+          // its O and l are zero, so any factor will do.
+          const bool fresh = m == -INFINITY;
+          const bool late = masked || __any_sync(0xffffffffu, fresh);
+          const float mref = fresh ? 0.f : m;
+          // -slope2 * (qpos - (key0 + c)) - mref for column c
+          const float base = fmaf(-slope2, float(qpos - key0), -mref);
+          const bool capped = a.score.cap_out > 0.f;
+          const float most = capped ? largest(x) : 0.f;
+          const bool small = !__any_sync(0xffffffffu, !(most <= a.cap.small));
+          psum = 0.f;
+          auto run = [&](auto&& f) {
+            using F = std::remove_reference_t<decltype(f)>;
+            auto form = [&](auto&& score) {
+              if (late) {
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 2) F::put(x, c, score(c));
+              } else {  // exponentials at once, interleaved with the scores' FMAs
+                psum = write_p(false, [&](int c) {
+                  const float2 y = score(c);
+                  F::put(x, c, y);
+                  return y;
+                });
+              }
+            };
+            if (!capped) {
+              form([&](int c) { return f.uncapped(a, c, raw(c)); });
+            } else if (small) {
+              form([&](int c) { return f.small(a.cap, c, raw(c)); });
+            } else {
+              f.large(a, x, !__any_sync(0xffffffffu, !(most <= a.cap.mid)));
+              if (!late) psum = write_p(false, raw);
+            }
+          };
+          if (a.score.slopes) run(OptionScores<true>(slope2, base));
+          else run(OptionScores<false>(slope2, base));
+          if (masked) mask();
+          const float tmax = tile_max();
+          const bool moved = tmax > (fresh ? -INFINITY : kSlack);
+          const float delta = moved ? tmax : 0.f;
+          const bool any_moved = __any_sync(0xffffffffu, moved);
+          if (moved) {
+            alpha = fresh ? 0.f : fast_exp2(-delta);
+            m = mref + delta;
+          }
+          if (late || any_moved) {
+            if (!late) tc::tmem_wait_st();  // the first P writes are done before they are replaced
+            // O holds every earlier tile: S(kt) completing means P V(kt - 1) has
+            if (kt > 0 && any_moved) rescale_o(alpha);
+            const float2 nd2 = make_float2(-delta, -delta);
+            psum = write_p(false, [&](int c) { return __fadd2_rn(raw(c), nd2); });
+          }
+        } else if (kt == 0 || masked) {
           const float tmax = tile_max();
           const bool moved = tmax > m + kSlack;
           const float mnew = moved ? tmax : m;
           alpha = moved ? fast_exp2(m - mnew) : 1.f;  // m = -inf -> 0
           if (kt > 0 && __any_sync(0xffffffffu, moved)) {
             // O holds every earlier tile: S(kt) completing means P V(kt - 1) has
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              float ov[32];
-              tc::tmem_ld32(lane_addr + col_o + 32 * c, ov);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-              tc::tmem_st32(lane_addr + col_o + 32 * c, ov);
-            }
+            rescale_o(alpha);
           }
-          psum = write_p(mnew, false);
+          psum = write_p(false, scaled(mnew));
           m = mnew;
         } else {
-          psum = write_p(m, true);
+          psum = write_p(true, scaled(m));
           const float tmax = tile_max();
           const bool moved = tmax > m + kSlack;
           if (__any_sync(0xffffffffu, moved)) {
             const float mnew = moved ? tmax : m;
             alpha = moved ? fast_exp2(m - mnew) : 1.f;
             tc::tmem_wait_st();  // the first P writes are done before they are replaced
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              float ov[32];
-              tc::tmem_ld32(lane_addr + col_o + 32 * c, ov);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-              tc::tmem_st32(lane_addr + col_o + 32 * c, ov);
-            }
-            psum = write_p(mnew, true);
+            rescale_o(alpha);
+            psum = write_p(true, scaled(mnew));
             m = mnew;
           }
         }
@@ -779,6 +855,7 @@ int launch_prefill(const pa_plan_s& plan, const RunPointers& p, void* stream) {
   if (p.options) {
     a.check = check;
     set_score_args(*p.options, &a.score, &a.score_scale);
+    a.cap = make_cap_poly(a.score, a.score_scale);
     return int(pr.dtype == PA_BF16 ? launch_t<BF16, kOptions>(a, tq, tk, tv, grid, s)
                                    : launch_t<F16, kOptions>(a, tq, tk, tv, grid, s));
   }

@@ -13,6 +13,7 @@ import ctypes
 import os
 
 import numpy as np
+import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpagedattn.so")
 if not os.path.exists(_LIB_PATH):
@@ -127,9 +128,8 @@ def _ptr(x):
 
 
 def _stream(s):
-    if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+    if s is None:  # torch's current stream of the current device
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -9,6 +9,8 @@ kernels.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import pagedattn as C
@@ -32,16 +34,25 @@ def _require(ok, what):
         raise ValueError(what)
 
 
-def _check_scales(scales, num_pages, page_size, num_kv_heads, scale_block, device, name):
-    _require(scales.dtype == torch.float32 and scales.device == device and scales.is_contiguous(),
-             f"{name}: a contiguous float32 tensor on {device}")
-    _require(scales.numel() == num_pages * page_size // scale_block * num_kv_heads,
-             f"{name}: one scale for each block of {scale_block} tokens and kv head "
-             f"([num_pages * page_size / scale_block, num_kv_heads])")
+def _check_scales(k_scales, v_scales, blocks, num_kv_heads, device):
+    n = blocks * num_kv_heads
+    for scales in (k_scales, v_scales):
+        if not (scales.dtype == torch.float32 and scales.device == device
+                and scales.numel() == n and scales.is_contiguous()):
+            raise ValueError(f"k_scales and v_scales: contiguous float32 [{blocks}, "
+                             f"{num_kv_heads}] (blocks of tokens of the pool, kv heads) on "
+                             f"{device}")
 
 
-def _attention_options(problem, device, k_pool, v_pool, k_scales, v_scales, scale_block,
-                       logit_cap, alibi_slopes):
+def _on(device):
+    """Makes ``device`` current for a launch (nothing to do if it is)."""
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _attention_options(problem, device, k_pool, k_scales, v_scales, scale_block, logit_cap,
+                       alibi_slopes):
     """The run's ``pa_attention_options``, or None if nothing is asked for."""
     if k_scales is None and v_scales is None and scale_block is None:
         if alibi_slopes is None and not logit_cap:
@@ -53,14 +64,13 @@ def _attention_options(problem, device, k_pool, v_pool, k_scales, v_scales, scal
             scale_block = problem.page_size
         _require(scale_block > 0 and problem.page_size % scale_block == 0,
                  "scale_block divides the page")
-        pages = k_pool.numel() // (problem.page_size * problem.num_kv_heads * problem.head_dim)
-        for name, scales in (("k_scales", k_scales), ("v_scales", v_scales)):
-            _check_scales(scales, pages, problem.page_size, problem.num_kv_heads, scale_block,
-                          device, name)
+        heads = problem.num_kv_heads
+        _check_scales(k_scales, v_scales,
+                      k_pool.numel() // (heads * problem.head_dim) // scale_block, heads, device)
     if alibi_slopes is not None:
-        _require(alibi_slopes.dtype == torch.float32 and alibi_slopes.device == device
-                 and alibi_slopes.is_contiguous() and alibi_slopes.numel() == problem.num_qo_heads,
-                 f"alibi_slopes: float32 on {device}, one per query head")
+        if not (alibi_slopes.dtype == torch.float32 and alibi_slopes.device == device
+                and alibi_slopes.numel() == problem.num_qo_heads and alibi_slopes.is_contiguous()):
+            raise ValueError(f"alibi_slopes: contiguous float32 on {device}, one per query head")
     return C.make_options(k_scales=k_scales, v_scales=v_scales, scale_block=scale_block,
                           logit_cap=logit_cap, alibi_slopes=alibi_slopes)
 
@@ -121,8 +131,8 @@ class PagedDecode:
         writes them.  ``logit_cap``: scores become ``cap * tanh(s / cap)``;
         ``alibi_slopes`` (float32 ``[num_qo_heads]``): scores lose slope *
         distance.  None of them goes with a shared prefix."""
-        options = _attention_options(self.problem, self.device, k_pool, v_pool, k_scales,
-                                     v_scales, scale_block, logit_cap, alibi_slopes)
+        options = _attention_options(self.problem, self.device, k_pool, k_scales, v_scales,
+                                     scale_block, logit_cap, alibi_slopes)
         _require(options is None or not self.prefix_len, "a cascade run takes no options")
         if o is None:
             o = torch.empty(self.batch, self.num_qo_heads, self.head_dim,
@@ -134,7 +144,7 @@ class PagedDecode:
             C.pa_cascade_run(self.plan, q, k_pool, v_pool, prefix_indices, kv_indices, o, lse,
                              self.workspace, self.workspace.numel(), stream)
         elif options is not None:
-            with torch.cuda.device(self.device):
+            with _on(self.device):
                 C.pa_run_options(self.plan, options, q, k_pool, v_pool, kv_indices, o, lse,
                                  self.workspace, self.workspace.numel(), stream)
         else:
@@ -186,7 +196,7 @@ class PagedPrefill:
             alibi_slopes=None):
         """``logit_cap`` and ``alibi_slopes`` as for ``PagedDecode.run``; slopes
         need the causal mask."""
-        options = _attention_options(self.problem, self.device, k_pool, v_pool, None, None, None,
+        options = _attention_options(self.problem, self.device, k_pool, None, None, None,
                                      logit_cap, alibi_slopes)
         if o is None:
             o = torch.empty(self.total_q, self.num_qo_heads, self.head_dim,
@@ -195,7 +205,7 @@ class PagedPrefill:
             lse = torch.empty(self.total_q, self.num_qo_heads, dtype=torch.float32,
                               device=self.device)
         if options is not None:
-            with torch.cuda.device(self.device):
+            with _on(self.device):
                 C.pa_prefill_run_options(self.plan, options, q, k_pool, v_pool, kv_indices, o,
                                          lse, self.workspace, self.workspace.numel(), stream)
         else:
@@ -242,44 +252,51 @@ class PagedKV:
         self.plan = C.pa_kv_plan_create(self.problem, self.scale_block, qo_indptr, kv_indptr,
                                         last_page_len)
         self.workspace_bytes = C.pa_plan_workspace_bytes(self.plan)
-        with torch.cuda.device(self.device):
+        with _on(self.device):
             self.workspace = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8,
                                          device=self.device)
             C.pa_plan_upload(self.plan, self.workspace, self.workspace.numel(), stream)
 
     def _check_cache(self, k_pool, v_pool, k_scales, v_scales, kv_indices):
-        n = self.num_pages * self.page_size * self.num_kv_heads * self.head_dim
-        for name, pool in (("k_pool", k_pool), ("v_pool", v_pool)):
-            _require(pool.dtype in (torch.uint8, _KV8_DTYPES[self.kv_dtype])
-                     and pool.device == self.device and pool.is_contiguous()
-                     and pool.numel() == n,
-                     f"{name}: contiguous {self.kv_dtype} codes "
-                     "[num_pages, page_size, num_kv_heads, 128] on the plan's device")
-        for name, scales in (("k_scales", k_scales), ("v_scales", v_scales)):
-            _check_scales(scales, self.num_pages, self.page_size, self.num_kv_heads,
-                          self.scale_block, self.device, name)
-        self._check_indices(kv_indices, "kv_indices")
+        device, row = self.device, self.num_kv_heads * self.head_dim
+        n = self.num_pages * self.page_size * row
+        for pool in (k_pool, v_pool):
+            if not ((pool.dtype == torch.uint8 or pool.dtype == _KV8_DTYPES[self.kv_dtype])
+                    and pool.device == device and pool.numel() == n and pool.is_contiguous()):
+                raise ValueError(f"k_pool and v_pool: contiguous {self.kv_dtype} codes "
+                                 f"[{self.num_pages}, {self.page_size}, {self.num_kv_heads}, "
+                                 f"{self.head_dim}] on {device}")
+        _check_scales(k_scales, v_scales, self.num_pages * self.page_size // self.scale_block,
+                      self.num_kv_heads, device)
+        self._check_indices(kv_indices)
 
-    def _check_indices(self, indices, name):
-        _require(indices.dtype == torch.int32 and indices.device == self.device
-                 and indices.is_contiguous() and indices.numel() >= self.total_pages,
-                 f"{name}: contiguous int32, one entry per page of the plan")
+    def _check_indices(self, indices):
+        if not (indices.dtype == torch.int32 and indices.device == self.device
+                and indices.numel() >= self.total_pages and indices.is_contiguous()):
+            raise ValueError(f"page indices: contiguous int32 on {self.device}, one for each of "
+                             f"the plan's {self.total_pages} pages")
 
-    def _check_rows(self, x, name):
-        _require(x.dtype == _TORCH_DTYPES[self.dtype] and x.device == self.device
-                 and x.shape == (self.total_q, self.num_kv_heads, self.head_dim)
-                 and x.stride(2) == 1 and x.stride(1) == self.head_dim,
-                 f"{name}: {self.dtype} rows [total_q, num_kv_heads, 128], heads packed")
-        # a single row has no next one to be apart from
-        return x.stride(0) if self.total_q > 1 else self.num_kv_heads * self.head_dim
+    def _row_strides(self, k, v):
+        """Checks the 16-bit rows; elements between the rows of each."""
+        shape = (self.total_q, self.num_kv_heads, self.head_dim)
+        out = []
+        for x in (k, v):
+            strides = x.stride()
+            if not (x.dtype == _TORCH_DTYPES[self.dtype] and x.device == self.device
+                    and x.shape == shape and strides[2] == 1 and strides[1] == self.head_dim):
+                raise ValueError(f"k and v: {self.dtype} rows {list(shape)} on {self.device}, "
+                                 "the heads of a row packed")
+            # a single row has no next one to be apart from
+            out.append(strides[0] if self.total_q > 1 else self.num_kv_heads * self.head_dim)
+        return out
 
     def append(self, k, v, k_pool, v_pool, k_scales, v_scales, kv_indices, stream=None):
         """Quantise the plan's tokens (``k``, ``v``: ``[total_q, num_kv_heads,
         128]``, rows at any stride that is a multiple of 8) into the pools and
         scales, in place."""
         self._check_cache(k_pool, v_pool, k_scales, v_scales, kv_indices)
-        ks, vs = self._check_rows(k, "k"), self._check_rows(v, "v")
-        with torch.cuda.device(self.device):
+        ks, vs = self._row_strides(k, v)
+        with _on(self.device):
             C.pa_kv_append(self.plan, k, ks, v, vs, k_pool, v_pool, k_scales, v_scales,
                            kv_indices, self.workspace, self.workspace.numel(), stream)
 
@@ -292,14 +309,14 @@ class PagedKV:
         row = self.num_kv_heads * self.head_dim
         out_pages = 0
         if out_indices is not None:
-            self._check_indices(out_indices, "out_indices")
+            self._check_indices(out_indices)
             shape = (self.page_size, self.num_kv_heads, self.head_dim)
-            for name, x in (("k", k), ("v", v)):
+            for x in (k, v):
                 _require(x is not None and x.dtype == _TORCH_DTYPES[self.dtype]
                          and x.device == self.device and x.is_contiguous() and x.dim() == 4
                          and x.shape[1:] == shape,
-                         f"{name}: a contiguous {self.dtype} pool "
-                         "[pages, page_size, num_kv_heads, 128] to unpack into")
+                         "k and v: contiguous 16-bit pools [pages, page_size, num_kv_heads, 128] "
+                         "to unpack into")
             _require(k.shape == v.shape, "k and v pools of the same size")
             ks = vs = row
             out_pages = k.shape[0]
@@ -309,12 +326,12 @@ class PagedKV:
                 k = torch.empty(shape, dtype=_TORCH_DTYPES[self.dtype], device=self.device)
             if v is None:
                 v = torch.empty(shape, dtype=_TORCH_DTYPES[self.dtype], device=self.device)
-            ks, vs = self._check_rows(k, "k"), self._check_rows(v, "v")
-        with torch.cuda.device(self.device):
+            ks, vs = self._row_strides(k, v)
+        with _on(self.device):
             C.pa_kv_read(self.plan, k_pool, v_pool, k_scales, v_scales, kv_indices, k, ks, v, vs,
                          out_indices, out_pages, self.workspace, self.workspace.numel(), stream)
         return k, v
 
     def check(self, stream=None) -> int:
-        with torch.cuda.device(self.device):
+        with _on(self.device):
             return C.pa_plan_check(self.plan, self.workspace, stream)
