@@ -54,7 +54,9 @@
 // S, softmax, P V, refill) took 3,111 cycles a tile of the ragged batch where
 // HBM needs 2,800.  Block scales ride ahead of their K rows: each loader lane
 // copies its tokens' K and V scale with 4-byte cp.async into one of four slots
-// with a barrier each.  Slot t % 4 is refilled for tile t + 4 after V(t + 3),
+// with a barrier each.  (Loaded into registers a step ahead and stored, they
+// cost the ragged batch 140 us for 128; only scattered ones, a scale per
+// one-token page, took 77 us for 81.)  Slot t % 4 is refilled for tile t + 4 after V(t + 3),
 // so after P V(t), which the softmax's reading of tile t precedes.  The K scale
 // multiplies the token's scores; the V scale v enters through the weights,
 // w = 2^(s - m) v in P's place, with the lazy reference m kept on s + log2 v,
@@ -357,6 +359,13 @@ template <typename Tag>
 __device__ __forceinline__ void write_out(const TcArgs& a, int64_t row, int d, float o, float lse2) {
   a.o[row * D + d] = from_float(Tag{}, o);
   if (d == 0 && a.lse) a.lse[row] = lse2 == -INFINITY ? -INFINITY : lse2 * kLn2;
+}
+
+// Maximum over the warp, one instruction (sm_100a); a NaN does not count.
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 __device__ __forceinline__ void flag_timeout(const TcArgs& a) { atomicOr(a.error_pos + 1, 1ull); }
@@ -910,11 +919,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
             }
           }
 #pragma unroll
-          for (int h = 0; h < kHalves; ++h) {
-            const float dist = qpos - float(it.token_begin + tt * kTT + kTok * h + i);
+          for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-            for (int hh = 0; hh < G; ++hh)
-              sv[h][hh] = final_score(sv[h][hh] * kscale[h] * scl[hh], a.score, slope2[hh], dist);
+            for (int hh = 0; hh < G; ++hh) sv[h][hh] *= kscale[h] * scl[hh];
+          if (a.score.cap_out > 0.f) {
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+              for (int hh = 0; hh < G; ++hh)
+                sv[h][hh] = a.score.cap_out * tanh_score(sv[h][hh]);
+          }
+          if (a.score.slopes) {
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+              const float dist = qpos - float(it.token_begin + tt * kTT + kTok * h + i);
+#pragma unroll
+              for (int hh = 0; hh < G; ++hh) sv[h][hh] = fmaf(-slope2[hh], dist, sv[h][hh]);
+            }
           }
         }
         // tile maximum per head over the tile's tokens: shuffles, then the 4 warps
@@ -925,8 +946,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
 #pragma unroll
           for (int h = 0; h < kHalves; ++h)
             v = fmaxf(v, !valid[h] ? -INFINITY : kExt ? sv[h][hh] + lv[h] : sv[h][hh]);
+          if constexpr (kExt) {
+            v = warp_max(v);
+          } else {
 #pragma unroll
-          for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+            for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+          }
           if (lane == 0) xm[warp * kN + hh] = v;
         }
         if (lane == 0) mbar_arrive(bar(kBarXReady + sbuf));
