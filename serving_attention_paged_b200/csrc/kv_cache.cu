@@ -21,8 +21,8 @@
 // neighbouring 256-byte rows.  Blocks of up to 16 tokens: a warp per unit,
 // 16 lanes per row, eight 16-byte loads per lane in flight, the row kept in
 // registers between the maximum and the rounding: each byte is read once.
-// Larger blocks: a 256-thread CTA per unit, 128 rows at a time in registers
-// (rows of a longer block are read a second time for the rounding, out of L2).
+// Larger blocks: a CTA per unit, up to 128 rows at a time in registers (rows of
+// a longer block are read a second time for the rounding, out of L2).
 // Both are bound by HBM; a decode step's few tokens by the launch and the
 // chain span -> page index -> row.  No atomics on results: a block's scale is
 // decided by one warp or CTA.
@@ -42,7 +42,6 @@ constexpr int D = kHeadDim;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSteps = 8;                      // row pairs a warp holds: 16 tokens
-constexpr int kChunk = 2 * kSteps * kWarps;    // rows a CTA holds: 128
 constexpr uint32_t kNoRow = 0xffffffffu;       // pool rows are < 2^32 - 1
 
 struct KvArgs {
@@ -55,8 +54,9 @@ struct KvArgs {
   const KvSpan* spans;
   unsigned long long* error_pos;
   int64_t num_pages, num_out_pages;
-  int64_t n_units;
-  int32_t num_kv_heads, log2_page, log2_block;
+  uint32_t n_units;  // the plan keeps it below 2^31
+  uint32_t num_kv_heads;
+  int32_t log2_page, log2_block;
   bool check;
 };
 
@@ -91,21 +91,35 @@ __device__ __forceinline__ void from_fp8x8(const uint2& u, float (&y)[8]) {
   }
 }
 
-// Largest finite |x| of 8 values as fp32 bits (which order as the values do);
-// 0 without a finite value.
+// Largest |x| of a run of 16-bit values, as its bits without the sign: they
+// order as the values do, two to a register, so 8 values take 4 masks and 2
+// three-way maxima.  Infinities and NaN order above every finite value; only
+// where one turns up is the maximum taken again without them (finite_amax).
+template <typename Tag> struct Half;
+template <> struct Half<F16> { static constexpr uint32_t kInf = 0x7c00u; };
+template <> struct Half<BF16> { static constexpr uint32_t kInf = 0x7f80u; };
+__device__ __forceinline__ uint32_t amax2(const uint4& u, uint32_t m) {
+  constexpr uint32_t kAbs = 0x7fff7fffu;
+  return __vimax3_u16x2(__vimax3_u16x2(m, u.x & kAbs, u.y & kAbs), u.z & kAbs, u.w & kAbs);
+}
+__device__ __forceinline__ uint32_t fold2(uint32_t m) { return max(m & 0xffffu, m >> 16); }
 template <typename Tag>
-__device__ __forceinline__ uint32_t amax_bits(const uint4& u, uint32_t m) {
-  float f[8];
-  to_float8(Tag{}, u, f);
+__device__ __forceinline__ uint32_t finite_amax(const uint4& u, uint32_t m) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t b = __float_as_uint(f[e]) & 0x7fffffffu;
-    m = max(m, b < 0x7f800000u ? b : 0u);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+    m = max(m, max(lo < Half<Tag>::kInf ? lo : 0u, hi < Half<Tag>::kInf ? hi : 0u));
   }
   return m;
 }
+template <typename Tag>
+__device__ __forceinline__ uint32_t as_fp32(uint32_t bits) {
+  return __float_as_uint(to_float(Tag{}, uint16_t(bits)));
+}
 
-// The smallest power of two s in [2^-60, 2^60] with a <= MAX * s.  Writing
+// The smallest power of two s in [2^-60, 2^60] with a <= MAX * s, a given by
+// its fp32 bits.  Writing
 // a = (1 + f) 2^e: a <= 1.75 * 2^(kMaxExp - 1) s holds for s = 2^(e - kMaxExp
 // + 1) if 1 + f <= 1.75, else for twice that.  (A subnormal or zero a clamps.)
 template <typename F>
@@ -120,8 +134,13 @@ template <typename Tag, typename F>
 __device__ __forceinline__ uint2 quantise(const uint4& u, float s, float inv, bool pow2) {
   float f[8];
   to_float8(Tag{}, u, f);
+  if (pow2) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = pow2 ? f[e] * inv : __fdiv_rn(f[e], s);
+    for (int e = 0; e < 8; ++e) f[e] *= inv;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = __fdiv_rn(f[e], s);
+  }
   return fp8x8<F>(f);
 }
 __device__ __forceinline__ bool is_pow2(float s) {
@@ -161,13 +180,12 @@ __device__ __forceinline__ void rescale8(uint8_t* p, float ratio) {
 
 // Blocks of 2^kLB <= 16 tokens: a warp per (span of 16 tokens, K or V, head).
 template <typename Tag, typename F, int kLB>
-__global__ void __launch_bounds__(kThreads) kv_append_warp_kernel(const KvArgs a) {
-  const int64_t unit = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kThreads, 4) kv_append_warp_kernel(const KvArgs a) {
+  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (unit >= a.n_units) return;
   const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
-  const int h = int(unit % a.num_kv_heads);
-  const int64_t rest = unit / a.num_kv_heads;
-  const int kv = int(rest & 1);
+  const uint32_t rest = unit / a.num_kv_heads;
+  const int h = int(unit - rest * a.num_kv_heads), kv = int(rest & 1);
   const KvSpan sp = a.spans[rest >> 1];
 
   const uint16_t* x0 = a.x[kv] + h * D + c * 8;
@@ -194,25 +212,42 @@ __global__ void __launch_bounds__(kThreads) kv_append_warp_kernel(const KvArgs a
   float* scales = a.scales[kv];
   if (has_old) s_old = scales[scale_index(a, first_row, h)];
 
-  uint32_t m[kSteps];
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) m[i] = amax_bits<Tag>(x[i], 0u);
   // the scale of each step's row pair (kLB = 0: of this half's row)
   constexpr int kPer = kLB == 0 ? 1 : 1 << (kLB - 1);  // steps per block
+  uint32_t m[kSteps / kPer], most = 0;
+#pragma unroll
+  for (int j = 0; j < kSteps / kPer; ++j) {
+    m[j] = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) m[j] = amax2(x[j * kPer + i], m[j]);
+    m[j] = fold2(m[j]);
+    most = max(most, m[j]);
+  }
+  if (__any_sync(0xffffffffu, most >= Half<Tag>::kInf)) {
+#pragma unroll
+    for (int j = 0; j < kSteps / kPer; ++j) {
+      m[j] = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) m[j] = finite_amax<Tag>(x[j * kPer + i], m[j]);
+    }
+  }
+  if constexpr (kLB == 0) {  // over the 16 lanes of a row, two rows' 16-bit maxima at a time
+#pragma unroll
+    for (int j = 0; j < kSteps; j += 2) {
+      uint32_t v = m[j] | (m[j + 1] << 16);
+#pragma unroll
+      for (int off = 8; off >= 1; off >>= 1) v = __vmaxu2(v, __shfl_xor_sync(0xffffffffu, v, off));
+      m[j] = v & 0xffffu;
+      m[j + 1] = v >> 16;
+    }
+  }
   float s[kSteps / kPer];
   float s_first = 0.f;
 #pragma unroll
   for (int j = 0; j < kSteps / kPer; ++j) {
-    uint32_t mj = m[j * kPer];
-#pragma unroll
-    for (int i = 1; i < kPer; ++i) mj = max(mj, m[j * kPer + i]);
-    if constexpr (kLB == 0) {
-#pragma unroll
-      for (int off = 8; off >= 1; off >>= 1) mj = max(mj, __shfl_xor_sync(0xffffffffu, mj, off));
-    } else {
-      mj = __reduce_max_sync(0xffffffffu, mj);
-    }
-    s[j] = scale_for<F>(mj);
+    uint32_t mj = m[j];
+    if constexpr (kLB > 0) mj = __reduce_max_sync(0xffffffffu, mj);
+    s[j] = scale_for<F>(as_fp32<Tag>(mj));
     // the block's tokens are [b0, b0 + 2^kLB); those written start at w0
     const int b0 = sp.start + 2 * kPer * j + (kLB == 0 ? half : 0);
     const int w0 = max(b0, sp.begin);
@@ -245,23 +280,21 @@ __global__ void __launch_bounds__(kThreads) kv_append_warp_kernel(const KvArgs a
   }
 }
 
-// Blocks of 32 to 1024 tokens: a CTA per (block, K or V, head).  The block
-// divides the page, so its rows are consecutive.
-template <typename Tag, typename F>
-__global__ void __launch_bounds__(kThreads) kv_append_block_kernel(const KvArgs a) {
-  __shared__ uint32_t warp_max[kWarps];
-  const int64_t unit = blockIdx.x;
+// Blocks of 32 to 1024 tokens: a CTA per (block, K or V, head), of a warp per 16
+// tokens but at most 8, so that every thread has its eight loads in flight
+// whatever the block (64-token blocks: 8 warps of four loads each moved 3.9
+// TB/s, 4 warps of eight 5.7).  The block divides the page, so its rows are
+// consecutive.
+template <typename Tag, typename F, int kW>
+__global__ void __launch_bounds__(32 * kW) kv_append_block_kernel(const KvArgs a) {
+  constexpr int kChunk = 2 * kSteps * kW;  // rows held at a time
+  __shared__ uint32_t warp_max[kW];
+  const uint32_t unit = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
-  const int h = int(unit % a.num_kv_heads);
-  const int64_t rest = unit / a.num_kv_heads;
-  const int kv = int(rest & 1);
+  const uint32_t rest = unit / a.num_kv_heads;
+  const int h = int(unit - rest * a.num_kv_heads), kv = int(rest & 1);
   const KvSpan sp = a.spans[rest >> 1];
-  const uint32_t row0 = pool_row(a, a.kv_indices, a.num_pages, sp.page_begin, sp.start);
-  if (row0 == kNoRow) return;  // the whole CTA: its block lies on one page
 
-  float* scale = a.scales[kv] + scale_index(a, row0, h);
-  const bool has_old = sp.start < sp.begin;
-  const float s_old = has_old ? *scale : 0.f;
   const uint16_t* x0 = a.x[kv] + h * D + c * 8;
   const int64_t stride = a.stride[kv];
   const int q0 = (sp.begin - sp.start) / kChunk, q1 = (sp.end - 1 - sp.start) / kChunk;
@@ -269,31 +302,46 @@ __global__ void __launch_bounds__(kThreads) kv_append_block_kernel(const KvArgs 
   auto load = [&](int q) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const int t = sp.start + q * kChunk + (i * kWarps + warp) * 2 + half;
+      const int t = sp.start + q * kChunk + (i * kW + warp) * 2 + half;
       x[i] = t >= sp.begin && t < sp.end
                  ? __ldg(reinterpret_cast<const uint4*>(x0 + (sp.row + int64_t(t - sp.begin)) * stride))
                  : make_uint4(0, 0, 0, 0);
     }
   };
+  load(q0);  // in flight while the page is looked up
+  const uint32_t row0 = pool_row(a, a.kv_indices, a.num_pages, sp.page_begin, sp.start);
+  if (row0 == kNoRow) return;  // the whole CTA: its block lies on one page
+
+  float* scale = a.scales[kv] + scale_index(a, row0, h);
+  const bool has_old = sp.start < sp.begin;
+  const float s_old = has_old ? *scale : 0.f;
   uint32_t m = 0;
   for (int q = q0; q <= q1; ++q) {
-    load(q);
+    if (q > q0) load(q);
+    uint32_t mq = 0;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) m = amax_bits<Tag>(x[i], m);
+    for (int i = 0; i < kSteps; ++i) mq = amax2(x[i], mq);
+    mq = fold2(mq);
+    if (__any_sync(0xffffffffu, mq >= Half<Tag>::kInf)) {
+      mq = 0;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) mq = finite_amax<Tag>(x[i], mq);
+    }
+    m = max(m, mq);
   }
   m = __reduce_max_sync(0xffffffffu, m);
   if (lane == 0) warp_max[warp] = m;
   __syncthreads();  // every thread has read the old scale, too
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) m = max(m, warp_max[w]);
-  float s = scale_for<F>(m);
+  for (int w = 0; w < kW; ++w) m = max(m, warp_max[w]);
+  float s = scale_for<F>(as_fp32<Tag>(m));
   if (has_old) s = fmaxf(s, s_old);
   if (threadIdx.x == 0) *scale = s;
 
   uint8_t* pool = a.pool[kv] + c * 8;
   if (has_old && s > s_old) {
     const float ratio = __fdiv_rn(s_old, s);
-    for (int t = sp.start + warp * 2 + half; t < sp.begin; t += 2 * kWarps)
+    for (int t = sp.start + warp * 2 + half; t < sp.begin; t += 2 * kW)
       rescale8<F>(pool + code_offset(a, row0 + uint32_t(t - sp.start), h), ratio);
   }
   const float inv = __frcp_rn(s);
@@ -302,7 +350,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_block_kernel(const KvArgs 
     if (q < q1) load(q);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const int t = sp.start + q * kChunk + (i * kWarps + warp) * 2 + half;
+      const int t = sp.start + q * kChunk + (i * kW + warp) * 2 + half;
       if (t >= sp.begin && t < sp.end)
         *reinterpret_cast<uint2*>(pool + code_offset(a, row0 + uint32_t(t - sp.start), h)) =
             quantise<Tag, F>(x[i], s, inv, pow2);
@@ -322,12 +370,11 @@ __device__ __forceinline__ uint32_t pack16(BF16, float lo, float hi) {
 // A warp per (16 tokens, K or V, head): scale * code, rounded once.
 template <typename Tag, typename F>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvArgs a) {
-  const int64_t unit = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (unit >= a.n_units) return;
   const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
-  const int h = int(unit % a.num_kv_heads);
-  int64_t rest = unit / a.num_kv_heads;
-  const int kv = int(rest & 1);
+  uint32_t rest = unit / a.num_kv_heads;
+  const int h = int(unit - rest * a.num_kv_heads), kv = int(rest & 1);
   rest >>= 1;
   // 16-token pieces of a longer span
   const int log2_pieces = max(a.log2_block - 4, 0);
@@ -391,7 +438,7 @@ KvArgs make_args(const pa_plan_s& plan, const KvPointers& p) {
   a.error_pos = reinterpret_cast<unsigned long long*>(p.ws + plan.ws.error);
   a.num_pages = pr.num_pages;
   a.num_out_pages = p.num_out_pages;
-  a.n_units = int64_t(plan.kv_spans.size()) * 2 * pr.num_kv_heads;
+  a.n_units = uint32_t(plan.kv_spans.size()) * 2u * uint32_t(pr.num_kv_heads);
   a.num_kv_heads = pr.num_kv_heads;
   a.log2_page = plan.log2_page;
   while ((1 << a.log2_block) < plan.scale_block) ++a.log2_block;
@@ -401,14 +448,16 @@ KvArgs make_args(const pa_plan_s& plan, const KvPointers& p) {
 
 template <typename Tag, typename F>
 void launch_append(const KvArgs& a, cudaStream_t s) {
-  const unsigned ctas = unsigned((a.n_units + kWarps - 1) / kWarps);
+  const unsigned ctas = (a.n_units + kWarps - 1) / kWarps;
   switch (a.log2_block) {
     case 0: kv_append_warp_kernel<Tag, F, 0><<<ctas, kThreads, 0, s>>>(a); break;
     case 1: kv_append_warp_kernel<Tag, F, 1><<<ctas, kThreads, 0, s>>>(a); break;
     case 2: kv_append_warp_kernel<Tag, F, 2><<<ctas, kThreads, 0, s>>>(a); break;
     case 3: kv_append_warp_kernel<Tag, F, 3><<<ctas, kThreads, 0, s>>>(a); break;
     case 4: kv_append_warp_kernel<Tag, F, 4><<<ctas, kThreads, 0, s>>>(a); break;
-    default: kv_append_block_kernel<Tag, F><<<unsigned(a.n_units), kThreads, 0, s>>>(a);
+    case 5: kv_append_block_kernel<Tag, F, 2><<<a.n_units, 64, 0, s>>>(a); break;
+    case 6: kv_append_block_kernel<Tag, F, 4><<<a.n_units, 128, 0, s>>>(a); break;
+    default: kv_append_block_kernel<Tag, F, 8><<<a.n_units, 256, 0, s>>>(a);
   }
 }
 
@@ -430,7 +479,7 @@ int launch_kv_read(const pa_plan_s& plan, const KvPointers& p, void* stream) {
   KvArgs a = make_args(plan, p);
   if (a.n_units == 0) return 0;
   if (a.log2_block > 4) a.n_units <<= a.log2_block - 4;  // 16-token pieces of a span
-  const unsigned ctas = unsigned((a.n_units + kWarps - 1) / kWarps);
+  const unsigned ctas = (a.n_units + kWarps - 1) / kWarps;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = plan.prob.kv_dtype == PA_E4M3;
   if (plan.prob.dtype == PA_BF16)
