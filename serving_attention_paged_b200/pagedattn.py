@@ -120,9 +120,7 @@ def _check(status: int, where: str):
 
 def _ptr(x):
     """Device (or host) address of a tensor / integer / None."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 

@@ -34,24 +34,25 @@ def _require(ok, what):
         raise ValueError(what)
 
 
-def _check_scales(k_scales, v_scales, blocks, num_kv_heads, device):
+def _check_scales(k_scales, v_scales, blocks, num_kv_heads, dev):
     n = blocks * num_kv_heads
     for scales in (k_scales, v_scales):
-        if not (scales.dtype == torch.float32 and scales.device == device
+        if not (scales.dtype is torch.float32 and scales.get_device() == dev
                 and scales.numel() == n and scales.is_contiguous()):
             raise ValueError(f"k_scales and v_scales: contiguous float32 [{blocks}, "
                              f"{num_kv_heads}] (blocks of tokens of the pool, kv heads) on "
-                             f"{device}")
+                             f"cuda:{dev}")
 
 
-def _on(device):
-    """Makes ``device`` current for a launch (nothing to do if it is)."""
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _on(dev):
+    """Makes device ``dev`` current for a launch (nothing to do if it is)."""
+    return _HERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
 
 
-def _attention_options(problem, device, k_pool, k_scales, v_scales, scale_block, logit_cap,
+_HERE = contextlib.nullcontext()
+
+
+def _attention_options(problem, dev, k_pool, k_scales, v_scales, scale_block, logit_cap,
                        alibi_slopes):
     """The run's ``pa_attention_options``, or None if nothing is asked for."""
     if k_scales is None and v_scales is None and scale_block is None:
@@ -66,11 +67,11 @@ def _attention_options(problem, device, k_pool, k_scales, v_scales, scale_block,
                  "scale_block divides the page")
         heads = problem.num_kv_heads
         _check_scales(k_scales, v_scales,
-                      k_pool.numel() // (heads * problem.head_dim) // scale_block, heads, device)
+                      k_pool.numel() // (heads * problem.head_dim) // scale_block, heads, dev)
     if alibi_slopes is not None:
-        if not (alibi_slopes.dtype == torch.float32 and alibi_slopes.device == device
+        if not (alibi_slopes.dtype is torch.float32 and alibi_slopes.get_device() == dev
                 and alibi_slopes.numel() == problem.num_qo_heads and alibi_slopes.is_contiguous()):
-            raise ValueError(f"alibi_slopes: contiguous float32 on {device}, one per query head")
+            raise ValueError(f"alibi_slopes: contiguous float32 on cuda:{dev}, one per query head")
     return C.make_options(k_scales=k_scales, v_scales=v_scales, scale_block=scale_block,
                           logit_cap=logit_cap, alibi_slopes=alibi_slopes)
 
@@ -131,7 +132,7 @@ class PagedDecode:
         writes them.  ``logit_cap``: scores become ``cap * tanh(s / cap)``;
         ``alibi_slopes`` (float32 ``[num_qo_heads]``): scores lose slope *
         distance.  None of them goes with a shared prefix."""
-        options = _attention_options(self.problem, self.device, k_pool, k_scales, v_scales,
+        options = _attention_options(self.problem, self.device.index, k_pool, k_scales, v_scales,
                                      scale_block, logit_cap, alibi_slopes)
         _require(options is None or not self.prefix_len, "a cascade run takes no options")
         if o is None:
@@ -144,7 +145,7 @@ class PagedDecode:
             C.pa_cascade_run(self.plan, q, k_pool, v_pool, prefix_indices, kv_indices, o, lse,
                              self.workspace, self.workspace.numel(), stream)
         elif options is not None:
-            with _on(self.device):
+            with _on(self.device.index):
                 C.pa_run_options(self.plan, options, q, k_pool, v_pool, kv_indices, o, lse,
                                  self.workspace, self.workspace.numel(), stream)
         else:
@@ -196,7 +197,7 @@ class PagedPrefill:
             alibi_slopes=None):
         """``logit_cap`` and ``alibi_slopes`` as for ``PagedDecode.run``; slopes
         need the causal mask."""
-        options = _attention_options(self.problem, self.device, k_pool, None, None, None,
+        options = _attention_options(self.problem, self.device.index, k_pool, None, None, None,
                                      logit_cap, alibi_slopes)
         if o is None:
             o = torch.empty(self.total_q, self.num_qo_heads, self.head_dim,
@@ -205,7 +206,7 @@ class PagedPrefill:
             lse = torch.empty(self.total_q, self.num_qo_heads, dtype=torch.float32,
                               device=self.device)
         if options is not None:
-            with _on(self.device):
+            with _on(self.device.index):
                 C.pa_prefill_run_options(self.plan, options, q, k_pool, v_pool, kv_indices, o,
                                          lse, self.workspace, self.workspace.numel(), stream)
         else:
@@ -244,6 +245,7 @@ class PagedKV:
         self.num_kv_heads, self.page_size, self.head_dim = num_kv_heads, page_size, head_dim
         self.num_pages = num_pages
         self.scale_block = page_size if scale_block is None else scale_block
+        self._row_shape = (self.total_q, num_kv_heads, head_dim)
         self.problem = C.make_problem(batch=self.batch, num_qo_heads=num_kv_heads,
                                       num_kv_heads=num_kv_heads, head_dim=head_dim,
                                       page_size=page_size, dtype=dtype, sm_scale=1.0, num_sms=1,
@@ -251,43 +253,43 @@ class PagedKV:
                                       kv_dtype=kv_dtype)
         self.plan = C.pa_kv_plan_create(self.problem, self.scale_block, qo_indptr, kv_indptr,
                                         last_page_len)
+        self._pool_elements = num_pages * page_size * num_kv_heads * head_dim
+        self._scale_blocks = num_pages * page_size // self.scale_block
         self.workspace_bytes = C.pa_plan_workspace_bytes(self.plan)
-        with _on(self.device):
+        with _on(self.device.index):
             self.workspace = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8,
                                          device=self.device)
             C.pa_plan_upload(self.plan, self.workspace, self.workspace.numel(), stream)
 
     def _check_cache(self, k_pool, v_pool, k_scales, v_scales, kv_indices):
-        device, row = self.device, self.num_kv_heads * self.head_dim
-        n = self.num_pages * self.page_size * row
+        dev, code, n = self.device.index, _KV8_DTYPES[self.kv_dtype], self._pool_elements
         for pool in (k_pool, v_pool):
-            if not ((pool.dtype == torch.uint8 or pool.dtype == _KV8_DTYPES[self.kv_dtype])
-                    and pool.device == device and pool.numel() == n and pool.is_contiguous()):
+            if not ((pool.dtype is code or pool.dtype is torch.uint8)
+                    and pool.get_device() == dev and pool.numel() == n and pool.is_contiguous()):
                 raise ValueError(f"k_pool and v_pool: contiguous {self.kv_dtype} codes "
                                  f"[{self.num_pages}, {self.page_size}, {self.num_kv_heads}, "
-                                 f"{self.head_dim}] on {device}")
-        _check_scales(k_scales, v_scales, self.num_pages * self.page_size // self.scale_block,
-                      self.num_kv_heads, device)
+                                 f"{self.head_dim}] on {self.device}")
+        _check_scales(k_scales, v_scales, self._scale_blocks, self.num_kv_heads, dev)
         self._check_indices(kv_indices)
 
     def _check_indices(self, indices):
-        if not (indices.dtype == torch.int32 and indices.device == self.device
+        if not (indices.dtype is torch.int32 and indices.get_device() == self.device.index
                 and indices.numel() >= self.total_pages and indices.is_contiguous()):
             raise ValueError(f"page indices: contiguous int32 on {self.device}, one for each of "
                              f"the plan's {self.total_pages} pages")
 
     def _row_strides(self, k, v):
         """Checks the 16-bit rows; elements between the rows of each."""
-        shape = (self.total_q, self.num_kv_heads, self.head_dim)
+        dtype, dev, shape = _TORCH_DTYPES[self.dtype], self.device.index, self._row_shape
         out = []
         for x in (k, v):
             strides = x.stride()
-            if not (x.dtype == _TORCH_DTYPES[self.dtype] and x.device == self.device
-                    and x.shape == shape and strides[2] == 1 and strides[1] == self.head_dim):
+            if not (x.dtype is dtype and x.get_device() == dev and x.shape == shape
+                    and strides[2] == 1 and strides[1] == shape[2]):
                 raise ValueError(f"k and v: {self.dtype} rows {list(shape)} on {self.device}, "
                                  "the heads of a row packed")
             # a single row has no next one to be apart from
-            out.append(strides[0] if self.total_q > 1 else self.num_kv_heads * self.head_dim)
+            out.append(strides[0] if shape[0] > 1 else shape[1] * shape[2])
         return out
 
     def append(self, k, v, k_pool, v_pool, k_scales, v_scales, kv_indices, stream=None):
@@ -296,7 +298,7 @@ class PagedKV:
         scales, in place."""
         self._check_cache(k_pool, v_pool, k_scales, v_scales, kv_indices)
         ks, vs = self._row_strides(k, v)
-        with _on(self.device):
+        with _on(self.device.index):
             C.pa_kv_append(self.plan, k, ks, v, vs, k_pool, v_pool, k_scales, v_scales,
                            kv_indices, self.workspace, self.workspace.numel(), stream)
 
@@ -321,17 +323,16 @@ class PagedKV:
             ks = vs = row
             out_pages = k.shape[0]
         else:
-            shape = (self.total_q, self.num_kv_heads, self.head_dim)
             if k is None:
-                k = torch.empty(shape, dtype=_TORCH_DTYPES[self.dtype], device=self.device)
+                k = torch.empty(self._row_shape, dtype=_TORCH_DTYPES[self.dtype], device=self.device)
             if v is None:
-                v = torch.empty(shape, dtype=_TORCH_DTYPES[self.dtype], device=self.device)
+                v = torch.empty(self._row_shape, dtype=_TORCH_DTYPES[self.dtype], device=self.device)
             ks, vs = self._row_strides(k, v)
-        with _on(self.device):
+        with _on(self.device.index):
             C.pa_kv_read(self.plan, k_pool, v_pool, k_scales, v_scales, kv_indices, k, ks, v, vs,
                          out_indices, out_pages, self.workspace, self.workspace.numel(), stream)
         return k, v
 
     def check(self, stream=None) -> int:
-        with _on(self.device):
+        with _on(self.device.index):
             return C.pa_plan_check(self.plan, self.workspace, stream)
