@@ -62,7 +62,7 @@
 // bound by the FMA pipe (a packed FMA takes two of its cycles), so operations
 // per score are what counts: the bias is one FMA; a cap is cap * tanh as x
 // times a polynomial in x^2 with every factor folded into its coefficients
-// (6 operations, bias added by the last) while the warp's scores are below half
+// (5 operations, bias added by the last) while the warp's scores are below half
 // the cap, a longer polynomial up to the cap, two MUFU operations per score in
 // the rare tile beyond; and all exponentials stay on the MUFU unit.  With a
 // distance bias the key tiles run last to first: the bias falls away from the
@@ -133,6 +133,7 @@ constexpr int kBarQFull = 0, kBarQEmpty = kBarQFull + 2, kBarKFull = kBarQEmpty 
 constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 8 + 1024;  // + slack to align to 1 KB
 constexpr uint32_t kTmemCols = 512;
 constexpr float kSlack = 8.f;
+constexpr float kSumMax = 8192.f;  // options: a tile's sum of P that keeps the reference
 constexpr int kPolyPairsPer8 = 1;  // pairs of exponentials (of 8) on the FMA pipe
 constexpr float kLn2 = 0.6931471805599453f;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
@@ -226,9 +227,9 @@ struct OptionScores {
   }
   __device__ __forceinline__ float2 small(const CapPoly& cap, int c, float2 v) const {
     const float2 u = __fmul2_rn(v, v);
-    float2 p = make_float2(cap.k[4], cap.k[4]);
+    float2 p = make_float2(cap.k[3], cap.k[3]);
 #pragma unroll
-    for (int i = 3; i >= 0; --i) p = __ffma2_rn(p, u, make_float2(cap.k[i], cap.k[i]));
+    for (int i = 2; i >= 0; --i) p = __ffma2_rn(p, u, make_float2(cap.k[i], cap.k[i]));
     return __ffma2_rn(v, p, bias(c));
   }
   // any |v|; which branch a tile takes is uniform in the warp
@@ -563,15 +564,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kKeys; ++c) x[c] = key0 + c < lim ? x[c] : -INFINITY;
         };
         if (!kExt && masked) mask();
-        // P = 2^(score - ref) in the input type, 32 keys at a time: `score(c)` gives
-        // the pair of scores at column c and may put them into x on the way
-        auto write_p = [&](bool poly, auto&& score) -> float {
+        // P = 2^(score(c)) in the input type, 32 keys at a time, and its sum;
+        // prepare(c) runs a group of 32 ahead, between the exponentials
+        auto write_p = [&](bool poly, auto&& score, auto&& prepare) -> float {
           float2 ps2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) prepare(c);
 #pragma unroll
           for (int c16 = 0; c16 < kKeys / 32; ++c16) {
             uint32_t w[16], wl[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
+              if (c16 + 1 < kKeys / 32) prepare(32 * (c16 + 1) + 2 * e);
               const float2 a2 = score(32 * c16 + 2 * e);
               float2 p2;
               if (poly && (e & 7) < kPolyPairsPer8) {  // on the FMA pipe
@@ -597,6 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return t.x + t.y;
         };
         auto raw = [&](int c) { return make_float2(x[c], x[c + 1]); };
+        auto nothing = [](int) {};
         auto scaled = [&](float ref) {
           return [&, sc2 = make_float2(a.score_scale, a.score_scale),
                   nm2 = make_float2(-ref, -ref)](int c) { return __ffma2_rn(raw(c), sc2, nm2); };
@@ -644,12 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (late) {
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 2) F::put(x, c, score(c));
-              } else {  // exponentials at once, interleaved with the scores' FMAs
-                psum = write_p(false, [&](int c) {
-                  const float2 y = score(c);
-                  F::put(x, c, y);
-                  return y;
-                });
+              } else {  // exponentials at once, between the next scores' FMAs
+                psum = write_p(false, raw, [&](int c) { F::put(x, c, score(c)); });
               }
             };
             if (!capped) {
@@ -658,15 +659,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               form([&](int c) { return f.small(a.cap, c, raw(c)); });
             } else {
               f.large(a, x, !__any_sync(0xffffffffu, !(most <= a.cap.mid)));
-              if (!late) psum = write_p(false, raw);
+              if (!late) psum = write_p(false, raw, nothing);
             }
           };
           if (a.score.slopes) run(OptionScores<true>(slope2, base));
           else run(OptionScores<false>(slope2, base));
           if (masked) mask();
-          const float tmax = tile_max();
-          const bool moved = tmax > (fresh ? -INFINITY : kSlack);
-          const float delta = moved ? tmax : 0.f;
+          // Not late: P's sum bounds every p, so the reference stays while the sum
+          // does (p <= 2^13 is far inside fp16's and bf16's range) and the tile
+          // maximum is not needed; its 64 maxima took 450 cycles of a tile's 3,550.
+          bool moved = !late && !(psum <= kSumMax);
+          float delta = 0.f;
+          if (late || __any_sync(0xffffffffu, moved)) {
+            const float tmax = tile_max();
+            if (late) moved = tmax > (fresh ? -INFINITY : kSlack);
+            if (moved) delta = fresh ? tmax : fmaxf(tmax, 0.f);
+          }
           const bool any_moved = __any_sync(0xffffffffu, moved);
           if (moved) {
             alpha = fresh ? 0.f : fast_exp2(-delta);
@@ -677,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // O holds every earlier tile: S(kt) completing means P V(kt - 1) has
             if (kt > 0 && any_moved) rescale_o(alpha);
             const float2 nd2 = make_float2(-delta, -delta);
-            psum = write_p(false, [&](int c) { return __fadd2_rn(raw(c), nd2); });
+            psum = write_p(false, [&](int c) { return __fadd2_rn(raw(c), nd2); }, nothing);
           }
         } else if (kt == 0 || masked) {
           const float tmax = tile_max();
@@ -688,10 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // O holds every earlier tile: S(kt) completing means P V(kt - 1) has
             rescale_o(alpha);
           }
-          psum = write_p(false, scaled(mnew));
+          psum = write_p(false, scaled(mnew), nothing);
           m = mnew;
         } else {
-          psum = write_p(true, scaled(m));
+          psum = write_p(true, scaled(m), nothing);
           const float tmax = tile_max();
           const bool moved = tmax > m + kSlack;
           if (__any_sync(0xffffffffu, moved)) {
@@ -699,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             alpha = moved ? fast_exp2(m - mnew) : 1.f;
             tc::tmem_wait_st();  // the first P writes are done before they are replaced
             rescale_o(alpha);
-            psum = write_p(true, scaled(mnew));
+            psum = write_p(true, scaled(mnew), nothing);
             m = mnew;
           }
         }
