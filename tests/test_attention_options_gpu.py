@@ -394,3 +394,95 @@ def test_wrapper_refusals():
     for cap in (-1.0, float("nan"), float("inf"), 1e9, 1e-9):
         with pytest.raises(C.PagedAttnError):
             pd.run(*dev, logit_cap=cap)
+
+
+@pytest.mark.parametrize("kernel", ["cuda_cores", "tensor_cores"])
+def test_cap_over_one_scale_per_tensor(kernel):
+    """8-bit pools without block scales keep k_scale and v_scale."""
+    from serving_attention_paged_b200.wrapper import PagedDecode
+    w = W.make_workload("options", EDGE_LENS, num_qo_heads=8, num_kv_heads=2, page_size=16,
+                        dtype="bf16", seed=21, kv_dtype="e5m2", k_scale=0.37, v_scale=1.3)
+    t = w.materialize()
+    slopes = torch.exp2(-torch.arange(1, 9).float())
+    pd = PagedDecode(w.kv_indptr, w.last_page_len, num_qo_heads=8, num_kv_heads=2, page_size=16,
+                     dtype="bf16", sm_scale=w.sm_scale, num_pages=w.num_pages, kv_dtype="e5m2",
+                     k_scale=0.37, v_scale=1.3, flags=KERNELS[kernel], num_sms=3, ctas_per_sm=1,
+                     min_chunk_tokens=64)
+    o, lse = pd.run(t["q"].cuda(), t["k_pool"].cuda(), t["v_pool"].cuda(),
+                    t["kv_indices"].cuda(), logit_cap=4.0, alibi_slopes=slopes.cuda())
+    ref = cache.attention(t["q"], t["k_pool"], t["v_pool"], w.kv_indptr, w.kv_indices,
+                          w.last_page_len, num_qo_heads=8, num_kv_heads=2, page_size=16,
+                          dtype="bf16", sm_scale=w.sm_scale, fmt="e5m2", k_scale=0.37,
+                          v_scale=1.3, logit_cap=4.0, alibi_slopes=slopes)
+    assert_close(to_np(o), to_np(lse), *ref, "bf16", kernel)
+
+
+@pytest.mark.parametrize("kernel", ["cuda_cores", "tensor_cores"])
+def test_negative_scales(kernel):
+    c = Case([300, 5], 4, 16, "bf16", "e4m3", 4, seed=22)
+    for s in (c.k_scales, c.v_scales):
+        s[::3] *= -1
+    _close(c.run(c.plan(flags=KERNELS[kernel])), c.expected(), "bf16", kernel)
+
+
+@pytest.mark.parametrize("kernel", ["cuda_cores", "tensor_cores"])
+def test_many_small_weights_behind_a_sink(kernel):
+    """One token takes nine tenths of the weight, 30,000 share the rest: each
+    is 2^-18 of the largest, and together they move o by a tenth of V."""
+    P, L = 64, 30000
+    c = Case([L], 8, P, "bf16", "e4m3", P, hkv=1, seed=23, spread=0.0)
+    w = c.w
+    rows = cache._rows(0, w.kv_indptr, w.kv_indices, w.last_page_len, P)
+    # every key 0 but the first, whose score is ln(9 (L - 1)) on every head
+    c.pools[0].zero_()
+    q = cache._widen16(c.q, "bf16").reshape(8, 128)
+    key = np.linalg.pinv(q) @ np.full(8, np.log(9.0 * (L - 1)) / w.sm_scale)
+    c.k_scales[:] = 2.0 ** -4
+    c.pools[0].view(-1, 128)[int(rows[0])] = torch.from_numpy(cache.fp8_encode(key * 16, "e4m3"))
+    # values: the sink's 0, the others' all 1 (code 64 * scale 1/64)
+    c.v_scales[:] = 2.0 ** -6
+    c.pools[1][:] = int(cache.fp8_encode([64.0], "e4m3")[0])
+    c.pools[1].view(-1, 128)[int(rows[0])] = 0
+    ref = c.expected()
+    assert 0.02 < ref[0].mean() < 0.3
+    for kw in SPLITS:
+        o, lse = c.run(c.plan(flags=KERNELS[kernel], **kw))
+        # each weight is kept to half of 2^-21 of the largest one, 2^-4 of itself, and a rounding
+        # common to all equal weights; o is their mean: 2^-4 of 0.1 at most
+        assert np.abs(o - ref[0]).max() <= 2.0 ** -4 * ref[0].max() + 2.0 ** -9
+        assert np.abs(lse - ref[1]).max() <= 1e-3
+
+
+def test_prefill_after_masked_tiles_and_odd_lengths():
+    """New tokens around the 128-key tiles and the halves' bounds, so that a
+    half's rows see no key of the item's last tile, for every group."""
+    from serving_attention_paged_b200.wrapper import PagedPrefill
+    for group, qo in ((1, [129, 257, 128, 300]), (2, [65, 129, 1, 130]), (8, [17, 33, 31, 16])):
+        kv = [n + d for n, d in zip(qo, [0, 127, 128, 1])]
+        c = Case(kv, group, 8, "bf16", seed=24, qo=qo)
+        w = c.w
+        pf = PagedPrefill(w.qo_indptr, w.kv_indptr, w.last_page_len, num_qo_heads=w.num_qo_heads,
+                          num_kv_heads=2, page_size=8, dtype="bf16", sm_scale=w.sm_scale,
+                          num_pages=w.num_pages, num_sms=3)
+        for cap in (0.0, 3.0, 300.0):
+            got = c.run(pf, cap, True)
+            ref = c.expected(qo_indptr=w.qo_indptr, logit_cap=cap, alibi_slopes=c.slopes)
+            assert_close(*got, *ref, "bf16", f"G={group} cap={cap}")
+
+
+def test_options_on_another_stream():
+    c = Case([300, 41], 4, 16, "f16", "e4m3", 8, seed=25)
+    pd = c.plan()
+    dev = [c.q.cuda(), *[p.cuda() for p in c.pools], torch.from_numpy(c.w.kv_indices).cuda()]
+    kw = dict(k_scales=c.k_scales.cuda(), v_scales=c.v_scales.cuda(), scale_block=8)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    o, lse = torch.empty(2, 8, 128, dtype=torch.float16, device="cuda"), torch.empty(2, 8, device="cuda")
+    pd.run(*dev, o=o, lse=lse, stream=s, **kw)
+    s.synchronize()
+    ref = c.expected()
+    _close((to_np(o), to_np(lse)), ref, "f16", "stream argument")
+    with torch.cuda.stream(s):
+        o2, lse2 = pd.run(*dev, **kw)
+    s.synchronize()
+    _close((to_np(o2), to_np(lse2)), ref, "f16", "current stream")

@@ -310,3 +310,66 @@ def test_empty_plans_and_empty_batch():
                     num_pages=c.num_pages, scale_block=8)
     empty.append(c.x[0].cuda(), c.x[1].cuda(), *dev)
     assert empty.check() == -1
+
+
+def test_pool_offsets_past_32_bits():
+    """Rows whose byte offset passes 2^32: the last pages of a 5 GB pool."""
+    from serving_attention_paged_b200.wrapper import PagedDecode, PagedKV
+    P, hkv, n = 64, 8, 80000                    # 80,000 x 64 x 1 KB = 5.2 GB per pool
+    lens = [100, 33]
+    indptr, _, last = W.tables_from_lengths(lens, P)
+    idx = np.array([n - 1, n - 3, n - 2], dtype=np.int32)
+    pools = [torch.empty(n, P, hkv, 128, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.ones(n, hkv, device="cuda") for _ in range(2)]
+    before = [p[:4].clone() for p in pools]
+    qo = np.array([0, 100, 133], dtype=np.int32)
+    x = torch.randn(2, 133, hkv, 128, generator=torch.Generator().manual_seed(0)).bfloat16()
+    pk = PagedKV(qo, indptr, last, num_kv_heads=hkv, page_size=P, dtype="bf16", kv_dtype="e4m3",
+                 num_pages=n)
+    idx_d = torch.from_numpy(idx).cuda()
+    pk.append(x[0].cuda(), x[1].cuda(), *pools, *scales, idx_d)
+    back = pk.read(*pools, *scales, idx_d)
+    small = np.array([2, 0, 1], dtype=np.int32)  # the same pages, of a pool of three
+    for w in range(2):
+        codes, s = cache.kv_append(x[w], np.zeros((3, P, hkv, 128), np.uint8), np.ones((3, hkv)),
+                                   qo, indptr, small, last, page_size=P, scale_block=P,
+                                   dtype="bf16", fmt="e4m3")
+        ref = cache.kv_read(codes, s, indptr, small, last, page_size=P, scale_block=P,
+                            dtype="bf16", fmt="e4m3")
+        assert torch.equal(back[w].cpu(), torch.from_numpy(ref).bfloat16())
+        assert torch.equal(pools[w][:4], before[w])
+    q = torch.randn(2, 32, 128, generator=torch.Generator().manual_seed(1)).bfloat16()
+    args = [cache.kv_append(x[w], np.zeros((3, P, hkv, 128), np.uint8), np.ones((3, hkv)), qo,
+                            indptr, small, last, page_size=P, scale_block=P, dtype="bf16",
+                            fmt="e4m3") for w in range(2)]
+    ref = cache.attention(q, args[0][0], args[1][0], indptr, small, last, num_qo_heads=32,
+                          num_kv_heads=hkv, page_size=P, dtype="bf16", sm_scale=0.0884,
+                          fmt="e4m3", k_scales=args[0][1], v_scales=args[1][1], scale_block=P)
+    for flags in (2, 4):
+        pd = PagedDecode(indptr, last, num_qo_heads=32, num_kv_heads=hkv, page_size=P,
+                         dtype="bf16", sm_scale=0.0884, num_pages=n, kv_dtype="e4m3", flags=flags)
+        o, lse = pd.run(q.cuda(), *pools, idx_d, k_scales=scales[0], v_scales=scales[1])
+        assert np.abs(o.double().cpu().numpy() - ref[0]).max() <= 2e-3 + 2.0 ** -8 * 4.5
+        assert np.abs(lse.double().cpu().numpy() - ref[1]).max() <= 1e-3
+
+
+def test_two_plans_into_one_cache_and_a_given_stream():
+    """Two appends of different requests into one pool, one after the other on
+    another stream than the current one."""
+    c = Cache([40, 17, 90], [40, 17, 90], 16, 16, "f16", "e4m3", seed=31)
+    dev = c.device()
+    x = c.x.cuda()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    from serving_attention_paged_b200.wrapper import PagedKV
+    for b0, b1 in ((0, 1), (1, 3)):
+        p0, p1 = int(c.indptr[b0]), int(c.indptr[b1])
+        pk = PagedKV(c.qo[b0:b1 + 1] - c.qo[b0], c.indptr[b0:b1 + 1] - p0, c.last[b0:b1],
+                     num_kv_heads=2, page_size=16, dtype="f16", kv_dtype="e4m3",
+                     num_pages=c.num_pages, scale_block=16, stream=s)
+        rows = slice(int(c.qo[b0]), int(c.qo[b1]))
+        idx = torch.from_numpy(c.indices[p0:p1]).cuda()
+        torch.cuda.synchronize()
+        pk.append(x[0, rows], x[1, rows], *dev[:4], idx, stream=s)
+        s.synchronize()
+    _check_append(c, dev)
