@@ -120,17 +120,16 @@ def _check(status: int, where: str):
 
 def _ptr(x):
     """Device (or host) address of a tensor / integer / None."""
-    if x is None or isinstance(x, int):
+    try:
+        return x.data_ptr()
+    except AttributeError:
         return x
-    return x.data_ptr()
 
 
 def _stream(s):
     if s is None:  # torch's current stream of the current device
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    if isinstance(s, int):
-        return s
-    return s.cuda_stream
+    return s if isinstance(s, int) else s.cuda_stream
 
 
 def _host_i32(a) -> np.ndarray:
@@ -345,20 +344,23 @@ def pa_prefill_run_options(plan: Plan, options: pa_attention_options, q, k_pool,
 
 def pa_kv_append(plan: Plan, k, k_stride: int, v, v_stride: int, k_pool, v_pool, k_scales,
                  v_scales, kv_indices, workspace, workspace_bytes: int, stream=None):
-    _check(lib.pa_kv_append(plan.handle, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(k_pool),
-                            _ptr(v_pool), _ptr(k_scales), _ptr(v_scales), _ptr(kv_indices),
-                            _ptr(workspace), workspace_bytes, _stream(stream)),
-           "pa_kv_append")
+    p = _ptr
+    status = lib.pa_kv_append(plan.handle, p(k), k_stride, p(v), v_stride, p(k_pool), p(v_pool),
+                              p(k_scales), p(v_scales), p(kv_indices), p(workspace),
+                              workspace_bytes, _stream(stream))
+    if status:
+        _check(status, "pa_kv_append")
 
 
 def pa_kv_read(plan: Plan, k_pool, v_pool, k_scales, v_scales, kv_indices, k, k_stride: int, v,
                v_stride: int, out_indices, num_out_pages: int, workspace, workspace_bytes: int,
                stream=None):
-    _check(lib.pa_kv_read(plan.handle, _ptr(k_pool), _ptr(v_pool), _ptr(k_scales),
-                          _ptr(v_scales), _ptr(kv_indices), _ptr(k), k_stride, _ptr(v), v_stride,
-                          _ptr(out_indices), num_out_pages, _ptr(workspace), workspace_bytes,
-                          _stream(stream)),
-           "pa_kv_read")
+    p = _ptr
+    status = lib.pa_kv_read(plan.handle, p(k_pool), p(v_pool), p(k_scales), p(v_scales),
+                            p(kv_indices), p(k), k_stride, p(v), v_stride, p(out_indices),
+                            num_out_pages, p(workspace), workspace_bytes, _stream(stream))
+    if status:
+        _check(status, "pa_kv_read")
 
 
 def pa_run_static_workspace(plan: Plan, q, k_pool, v_pool, kv_indices, o, lse, stream=None):

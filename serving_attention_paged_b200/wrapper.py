@@ -36,9 +36,9 @@ def _require(ok, what):
 
 def _check_scales(k_scales, v_scales, blocks, num_kv_heads, dev):
     n = blocks * num_kv_heads
-    for scales in (k_scales, v_scales):
-        if not (scales.dtype is torch.float32 and scales.get_device() == dev
-                and scales.numel() == n and scales.is_contiguous()):
+    for x in (k_scales, v_scales):
+        if not (x.dtype is torch.float32 and x.numel() == n and x.get_device() == dev
+                and x.is_contiguous()):
             raise ValueError(f"k_scales and v_scales: contiguous float32 [{blocks}, "
                              f"{num_kv_heads}] (blocks of tokens of the pool, kv heads) on "
                              f"cuda:{dev}")
@@ -90,7 +90,7 @@ class PagedDecode:
                  piece_cost_tokens=0, kv_dtype=None, k_scale=1.0, v_scale=1.0,
                  rope_theta=0.0, stream=None):
         self.device = _device(device)
-        dev_index = self.device.index
+        self._dev = dev_index = self.device.index
         self.dtype = dtype
         self.batch = len(last_page_len)
         self.num_qo_heads, self.head_dim = num_qo_heads, head_dim
@@ -132,7 +132,7 @@ class PagedDecode:
         writes them.  ``logit_cap``: scores become ``cap * tanh(s / cap)``;
         ``alibi_slopes`` (float32 ``[num_qo_heads]``): scores lose slope *
         distance.  None of them goes with a shared prefix."""
-        options = _attention_options(self.problem, self.device.index, k_pool, k_scales, v_scales,
+        options = _attention_options(self.problem, self._dev, k_pool, k_scales, v_scales,
                                      scale_block, logit_cap, alibi_slopes)
         _require(options is None or not self.prefix_len, "a cascade run takes no options")
         if o is None:
@@ -145,7 +145,7 @@ class PagedDecode:
             C.pa_cascade_run(self.plan, q, k_pool, v_pool, prefix_indices, kv_indices, o, lse,
                              self.workspace, self.workspace.numel(), stream)
         elif options is not None:
-            with _on(self.device.index):
+            with _on(self._dev):
                 C.pa_run_options(self.plan, options, q, k_pool, v_pool, kv_indices, o, lse,
                                  self.workspace, self.workspace.numel(), stream)
         else:
@@ -168,6 +168,7 @@ class PagedPrefill:
                  page_size, dtype, sm_scale, num_pages, causal=True, head_dim=128, device=None,
                  num_sms=None, flags=0, stream=None):
         self.device = _device(device)
+        self._dev = self.device.index
         self.dtype = dtype
         self.batch = len(last_page_len)
         self.total_q = int(qo_indptr[-1]) if self.batch else 0
@@ -197,7 +198,7 @@ class PagedPrefill:
             alibi_slopes=None):
         """``logit_cap`` and ``alibi_slopes`` as for ``PagedDecode.run``; slopes
         need the causal mask."""
-        options = _attention_options(self.problem, self.device.index, k_pool, None, None, None,
+        options = _attention_options(self.problem, self._dev, k_pool, None, None, None,
                                      logit_cap, alibi_slopes)
         if o is None:
             o = torch.empty(self.total_q, self.num_qo_heads, self.head_dim,
@@ -206,7 +207,7 @@ class PagedPrefill:
             lse = torch.empty(self.total_q, self.num_qo_heads, dtype=torch.float32,
                               device=self.device)
         if options is not None:
-            with _on(self.device.index):
+            with _on(self._dev):
                 C.pa_prefill_run_options(self.plan, options, q, k_pool, v_pool, kv_indices, o,
                                          lse, self.workspace, self.workspace.numel(), stream)
         else:
@@ -236,6 +237,7 @@ class PagedKV:
                  kv_dtype, num_pages, scale_block=None, head_dim=128, device=None, flags=0,
                  stream=None):
         self.device = _device(device)
+        self._dev = self.device.index
         self.dtype, self.kv_dtype = dtype, kv_dtype
         self.batch = len(last_page_len)
         _require(len(qo_indptr) == self.batch + 1 and len(kv_indptr) == self.batch + 1,
@@ -246,6 +248,7 @@ class PagedKV:
         self.num_pages = num_pages
         self.scale_block = page_size if scale_block is None else scale_block
         self._row_shape = (self.total_q, num_kv_heads, head_dim)
+        self._row_dtype, self._code_dtype = _TORCH_DTYPES[dtype], _KV8_DTYPES[kv_dtype]
         self.problem = C.make_problem(batch=self.batch, num_qo_heads=num_kv_heads,
                                       num_kv_heads=num_kv_heads, head_dim=head_dim,
                                       page_size=page_size, dtype=dtype, sm_scale=1.0, num_sms=1,
@@ -256,51 +259,50 @@ class PagedKV:
         self._pool_elements = num_pages * page_size * num_kv_heads * head_dim
         self._scale_blocks = num_pages * page_size // self.scale_block
         self.workspace_bytes = C.pa_plan_workspace_bytes(self.plan)
-        with _on(self.device.index):
+        with _on(self._dev):
             self.workspace = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8,
                                          device=self.device)
-            C.pa_plan_upload(self.plan, self.workspace, self.workspace.numel(), stream)
+            self.workspace_size = self.workspace.numel()
+            C.pa_plan_upload(self.plan, self.workspace, self.workspace_size, stream)
 
     def _check_cache(self, k_pool, v_pool, k_scales, v_scales, kv_indices):
-        dev, code, n = self.device.index, _KV8_DTYPES[self.kv_dtype], self._pool_elements
-        for pool in (k_pool, v_pool):
-            if not ((pool.dtype is code or pool.dtype is torch.uint8)
-                    and pool.get_device() == dev and pool.numel() == n and pool.is_contiguous()):
+        dev, code, n = self._dev, self._code_dtype, self._pool_elements
+        for x in (k_pool, v_pool):
+            dtype = x.dtype
+            if not ((dtype is code or dtype is torch.uint8) and x.numel() == n
+                    and x.get_device() == dev and x.is_contiguous()):
                 raise ValueError(f"k_pool and v_pool: contiguous {self.kv_dtype} codes "
                                  f"[{self.num_pages}, {self.page_size}, {self.num_kv_heads}, "
                                  f"{self.head_dim}] on {self.device}")
         _check_scales(k_scales, v_scales, self._scale_blocks, self.num_kv_heads, dev)
         self._check_indices(kv_indices)
 
-    def _check_indices(self, indices):
-        if not (indices.dtype is torch.int32 and indices.get_device() == self.device.index
-                and indices.numel() >= self.total_pages and indices.is_contiguous()):
+    def _check_indices(self, x):
+        if not (x.dtype is torch.int32 and x.numel() >= self.total_pages
+                and x.get_device() == self._dev and x.is_contiguous()):
             raise ValueError(f"page indices: contiguous int32 on {self.device}, one for each of "
                              f"the plan's {self.total_pages} pages")
 
-    def _row_strides(self, k, v):
-        """Checks the 16-bit rows; elements between the rows of each."""
-        dtype, dev, shape = _TORCH_DTYPES[self.dtype], self.device.index, self._row_shape
-        out = []
-        for x in (k, v):
-            strides = x.stride()
-            if not (x.dtype is dtype and x.get_device() == dev and x.shape == shape
-                    and strides[2] == 1 and strides[1] == shape[2]):
-                raise ValueError(f"k and v: {self.dtype} rows {list(shape)} on {self.device}, "
-                                 "the heads of a row packed")
-            # a single row has no next one to be apart from
-            out.append(strides[0] if shape[0] > 1 else shape[1] * shape[2])
-        return out
+    def _row_stride(self, x):
+        """Checks 16-bit rows; elements from one to the next."""
+        rows, heads, d = self._row_shape
+        stride, inner, last = x.stride() if x.dim() == 3 else (0, 0, 0)
+        if not (last == 1 and inner == d and x.dtype is self._row_dtype
+                and x.shape == self._row_shape and x.get_device() == self._dev):
+            raise ValueError(f"k and v: {self.dtype} rows {list(self._row_shape)} on "
+                             f"{self.device}, the heads of a row packed")
+        # a single row has no next one to be apart from
+        return stride if rows > 1 else heads * d
 
     def append(self, k, v, k_pool, v_pool, k_scales, v_scales, kv_indices, stream=None):
         """Quantise the plan's tokens (``k``, ``v``: ``[total_q, num_kv_heads,
         128]``, rows at any stride that is a multiple of 8) into the pools and
         scales, in place."""
         self._check_cache(k_pool, v_pool, k_scales, v_scales, kv_indices)
-        ks, vs = self._row_strides(k, v)
-        with _on(self.device.index):
+        ks, vs = self._row_stride(k), self._row_stride(v)
+        with _on(self._dev):
             C.pa_kv_append(self.plan, k, ks, v, vs, k_pool, v_pool, k_scales, v_scales,
-                           kv_indices, self.workspace, self.workspace.numel(), stream)
+                           kv_indices, self.workspace, self.workspace_size, stream)
 
     def read(self, k_pool, v_pool, k_scales, v_scales, kv_indices, k=None, v=None,
              out_indices=None, stream=None):
@@ -327,12 +329,12 @@ class PagedKV:
                 k = torch.empty(self._row_shape, dtype=_TORCH_DTYPES[self.dtype], device=self.device)
             if v is None:
                 v = torch.empty(self._row_shape, dtype=_TORCH_DTYPES[self.dtype], device=self.device)
-            ks, vs = self._row_strides(k, v)
-        with _on(self.device.index):
+            ks, vs = self._row_stride(k), self._row_stride(v)
+        with _on(self._dev):
             C.pa_kv_read(self.plan, k_pool, v_pool, k_scales, v_scales, kv_indices, k, ks, v, vs,
-                         out_indices, out_pages, self.workspace, self.workspace.numel(), stream)
+                         out_indices, out_pages, self.workspace, self.workspace_size, stream)
         return k, v
 
     def check(self, stream=None) -> int:
-        with _on(self.device.index):
+        with _on(self._dev):
             return C.pa_plan_check(self.plan, self.workspace, stream)
