@@ -507,12 +507,14 @@ __device__ __forceinline__ void run_piece(const DecodeArgs& a, const pa_work_ite
   const PieceCopier<C, kCheckMode, kScaled> cp(a, it, smem, scale_ring);
   if (!started) cp.start(pg);
   // options: this lane's head's bias per unit of distance, and the distance
-  // to this thread's first token of the tile, less one tile per tile
-  float slope2 = 0.f, dist = 0.f;
+  // to this thread's first token of the tile (an integer: a long request's
+  // passes fp32's), less one tile per tile
+  float slope2 = 0.f;
+  int dist = 0;
   if constexpr (kExt) {
     if (a.score.slopes) {
       slope2 = __ldg(a.score.slopes + hq0 + my_head) * kLog2e;
-      dist = float(__ldg(a.kv_len + b) - 1 - (tb + grp));
+      dist = __ldg(a.kv_len + b) - 1 - (tb + grp);
     }
   }
 
@@ -537,6 +539,7 @@ __device__ __forceinline__ void run_piece(const DecodeArgs& a, const pa_work_ite
     read_off = read_off + C::kStageBytes == C::kRingBytes ? 0u : read_off + C::kStageBytes;
     const uint8_t* vs = ks + C::kHalfStage;
 
+    const float fdist = float(dist);
     float sc[TPG];
 #pragma unroll
     for (int j = 0; j < TPG; ++j) {
@@ -577,12 +580,12 @@ __device__ __forceinline__ void run_piece(const DecodeArgs& a, const pa_work_ite
       float r = reduce_scatter<G, LT>(part) * a.score_scale;
       if constexpr (kExt) {
         if constexpr (kScaled) r *= kscale[j];
-        r = final_score(r, a.score, slope2, dist - float(kGroups * j));
+        r = final_score(r, a.score, slope2, fdist - float(kGroups * j));
       }
       sc[j] = (t * kTile + grp + kGroups * j < len) ? r : -INFINITY;
     }
 
-    if constexpr (kExt) dist -= float(kTile);
+    if constexpr (kExt) dist -= kTile;
 
     // Lazy running max: the reference point m moves only when a score beats
     // it by more than kSlack (base 2), so p = 2^(s - m) <= 2^kSlack and o is

@@ -843,9 +843,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
       const int len = it.token_end - it.token_begin;
       const int ntiles = (len + kTT - 1) / kTT;
       if (ntiles == 0) continue;  // the epilogue warps write its (0, -inf)
-      float slope2[G], qpos = 0.f;  // options: bias per unit of distance, the query's position
+      float slope2[G];  // options: bias per unit of distance, and the query's position (an
+      int qpos = 0;     // integer: a long request's passes fp32's)
       if constexpr (kExt) {
-        if (a.score.slopes) qpos = float(__ldg(a.kv_len + it.request) - 1);
+        if (a.score.slopes) qpos = __ldg(a.kv_len + it.request) - 1;
 #pragma unroll
         for (int hh = 0; hh < G; ++hh)
           slope2[hh] = a.score.slopes ? __ldg(a.score.slopes + it.kv_head * G + hh) * kLog2e : 0.f;
@@ -932,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
           if (a.score.slopes) {
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
-              const float dist = qpos - float(it.token_begin + tt * kTT + kTok * h + i);
+              const float dist = float(qpos - (it.token_begin + tt * kTT + kTok * h + i));
 #pragma unroll
               for (int hh = 0; hh < G; ++hh) sv[h][hh] = fmaf(-slope2[hh], dist, sv[h][hh]);
             }

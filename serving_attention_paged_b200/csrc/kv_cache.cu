@@ -147,13 +147,14 @@ __device__ __forceinline__ bool is_pow2(float s) {
   return (__float_as_uint(s) & 0x7fffffu) == 0;  // normal, mantissa zero
 }
 
-// Pool row of request token t, kNoRow if the bounds check rejects its page.
+// Pool row of request token t, kNoRow if its page is negative or the bounds
+// check rejects it.
 __device__ __forceinline__ uint32_t pool_row(const KvArgs& a, const int32_t* indices,
                                              int64_t num_pages, int page_begin, int t) {
   const int pos = page_begin + (t >> a.log2_page);
   const int page = __ldg(indices + pos);
-  if (a.check && (page < 0 || int64_t(page) >= num_pages)) {
-    atomicMin(a.error_pos, (unsigned long long)pos);
+  if (page < 0 || (a.check && int64_t(page) >= num_pages)) {
+    if (a.check) atomicMin(a.error_pos, (unsigned long long)pos);
     return kNoRow;
   }
   return (uint32_t(page) << a.log2_page) | (uint32_t(t) & ((1u << a.log2_page) - 1u));

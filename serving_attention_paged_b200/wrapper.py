@@ -287,7 +287,7 @@ class PagedKV:
         """Checks 16-bit rows; elements from one to the next."""
         rows, heads, d = self._row_shape
         stride, inner, last = x.stride() if x.dim() == 3 else (0, 0, 0)
-        if not (last == 1 and inner == d and x.dtype is self._row_dtype
+        if not (last == 1 and (inner == d or heads == 1) and x.dtype is self._row_dtype
                 and x.shape == self._row_shape and x.get_device() == self._dev):
             raise ValueError(f"k and v: {self.dtype} rows {list(self._row_shape)} on "
                              f"{self.device}, the heads of a row packed")

@@ -486,3 +486,62 @@ def test_options_on_another_stream():
         o2, lse2 = pd.run(*dev, **kw)
     s.synchronize()
     _close((to_np(o2), to_np(lse2)), ref, "f16", "current stream")
+
+
+@pytest.mark.parametrize("kernel", ["cuda_cores", "tensor_cores"])
+@pytest.mark.parametrize("fmt", [None, "e4m3"])
+def test_distances_past_2_to_24(fmt, kernel):
+    """A request of 2^24 + 37 tokens (one page of zeros repeated, then a last
+    page of its own): keys 0, so the bias alone weighs, and the nearest
+    distances must be exact integers.  o and lse in closed form."""
+    from serving_attention_paged_b200.wrapper import PagedDecode
+    P, hkv, G, last = 1024, 1, 4, 37
+    n = (1 << 24) // P
+    L = n * P + last
+    indptr, indices = np.array([0, n + 1]), np.zeros(n + 1, np.int32)
+    indices[-1] = 1
+    slope = 0.25
+    v = torch.zeros(2, P, hkv, 128)
+    v[1, :last] = torch.randn(last, hkv, 128, generator=torch.Generator().manual_seed(4))
+    k = torch.zeros(2, P, hkv, 128)
+    kw = {}
+    if fmt:
+        v = torch.from_numpy(cache.fp8_encode(v.double().numpy() * 64, fmt))
+        values = cache.fp8_table(fmt)[v.numpy()] / 64
+        k = torch.zeros_like(v)
+        kw = dict(k_scales=torch.ones(2, hkv, device="cuda"), scale_block=P,
+                  v_scales=torch.full((2, hkv), 1 / 64, device="cuda"))
+    else:
+        k, v = k.bfloat16(), v.bfloat16()
+        values = v.double().numpy()
+    pd = PagedDecode(indptr, [last], num_qo_heads=hkv * G, num_kv_heads=hkv, page_size=P,
+                     dtype="bf16", sm_scale=0.1, num_pages=2, kv_dtype=fmt, flags=KERNELS[kernel])
+    q = torch.randn(1, hkv * G, 128, generator=torch.Generator().manual_seed(5)).bfloat16()
+    o, lse = pd.run(q.cuda(), k.cuda(), v.cuda(), torch.from_numpy(indices).cuda(),
+                    alibi_slopes=torch.full((G,), slope, device="cuda"), **kw)
+    w = np.exp(-slope * np.arange(last)[::-1])       # of the last page's tokens
+    z = (1 - np.exp(-slope * L)) / (1 - np.exp(-slope))
+    ref = (w[:, None] * values[1, :last, 0]).sum(0) / z
+    assert_close(to_np(o), to_np(lse), np.broadcast_to(ref, (1, G, 128)),
+                 np.full((1, G), np.log(z)), "bf16", kernel)
+
+
+def test_prefill_options_report_a_bad_page():
+    from serving_attention_paged_b200 import pagedattn as C
+    from serving_attention_paged_b200.wrapper import PagedPrefill
+    c = Case([100, 70], 4, 16, "bf16", seed=26, qo=[100, 20])
+    w = c.w
+    pf = PagedPrefill(w.qo_indptr, w.kv_indptr, w.last_page_len, num_qo_heads=8, num_kv_heads=2,
+                      page_size=16, dtype="bf16", sm_scale=w.sm_scale, num_pages=w.num_pages,
+                      flags=C.PA_FLAG_CHECK_INDICES)
+    idx = w.kv_indices.copy()
+    idx[3] = -2
+    o, lse = pf.run(c.q.cuda(), *[p.cuda() for p in c.pools], torch.from_numpy(idx).cuda(),
+                    logit_cap=10.0, alibi_slopes=c.slopes.cuda())
+    with pytest.raises(C.PagedAttnError) as e:
+        pf.check()
+    assert e.value.position == 3
+    page = int(w.kv_indices[3])
+    c.pools[0][page], c.pools[1][page] = 0, 0  # its tokens read as zeros
+    ref = c.expected(qo_indptr=w.qo_indptr, logit_cap=10.0, alibi_slopes=c.slopes)
+    assert_close(to_np(o), to_np(lse), *ref, "bf16", "bad page")

@@ -373,3 +373,29 @@ def test_two_plans_into_one_cache_and_a_given_stream():
         pk.append(x[0, rows], x[1, rows], *dev[:4], idx, stream=s)
         s.synchronize()
     _check_append(c, dev)
+
+
+def test_negative_pages_are_skipped_without_the_check():
+    c = Cache([40], [40], 16, 16, "f16", "e4m3", seed=41)
+    dev = c.device()
+    idx = c.indices.copy()
+    idx[1] = -1
+    c.plan().append(c.x[0].cuda(), c.x[1].cuda(), *dev[:4], torch.from_numpy(idx).cuda())
+    for w in range(2):
+        codes, scales = c.expected(w)
+        page = int(c.indices[1])
+        codes[page], scales[page] = c.codes[w][page].numpy(), c.scales[w][page].numpy()
+        assert np.array_equal(dev[w].cpu().numpy(), codes)
+        assert np.array_equal(dev[2 + w].cpu().numpy().astype(np.float64), scales)
+
+
+def test_single_head_rows_at_any_inner_stride():
+    """One kv head: the stride of the heads' axis says nothing."""
+    c = Cache([40, 3], [40, 3], 16, 16, "bf16", "e4m3", hkv=1, seed=42)
+    dev = c.device()
+    x = [torch.empty_strided((43, 1, 128), (128, 7, 1), dtype=torch.bfloat16, device="cuda")
+         for _ in range(2)]
+    for a, b in zip(x, c.x):
+        a.copy_(b)
+    c.plan().append(*x, *dev)
+    _check_append(c, dev)
