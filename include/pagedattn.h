@@ -19,14 +19,18 @@
  *     cores).
  *   - README, core feature 5: CUDA-graph capture.  pa_run, pa_cascade_run,
  *     pa_prefill_run and pa_merge_state only enqueue work on the given
- *     stream: no host synchronisation, no allocation.
+ *     stream: no host synchronisation, no allocation; so do pa_run_options,
+ *     pa_prefill_run_options, pa_kv_append and pa_kv_read.
  *   - flashinfer-cubin registry page, quickstart: the paged-table names
  *     kv_indptr, kv_indices, last_page_len and kv_layout (NHD here).
  *   - hysenlabs project review, "Installing FlashInfer and running a first
  *     decode": the decode example's query has shape [num_qo_heads, head_dim],
  *     its keys and values [kv_len, num_kv_heads, head_dim] (NHD).
  * The merge of partial states by log-sum-exp (pa_merge_state) is not named
- * on the pages; split-KV and cascade both need it.
+ * on the pages; split-KV and cascade both need it.  Neither are the cache's
+ * block scales, its writing and reading (pa_kv_append, pa_kv_read) or the
+ * capped and biased scores: they are what serving a model over a compressed
+ * cache (core feature 3) takes, to this library's own formulas.
  *
  * Math (per request b, q head hq, kv head h = hq / (Hq / Hkv)):
  *   L_b  = 0 if n_b = 0 else (n_b - 1) * P + last_page_len[b]
@@ -123,9 +127,11 @@ typedef struct {
    * key is k_scale * code, the value v_scale * code (one scale per tensor;
    * both finite and > 0).  q and o stay in `dtype`.  Any other kv_dtype
    * (PA_F16 / PA_BF16) means the pools hold `dtype` and the scales are unused.
-   * 8-bit caches run on the CUDA-core decode kernel (pa_run,
-   * pa_run_static_workspace); cascade plans with a prefix, prefill plans and
-   * PA_FLAG_TENSOR_CORES refuse them with PA_ERR_UNSUPPORTED. */
+   * 8-bit caches run on the tensor-core decode kernel, or with
+   * PA_FLAG_CUDA_CORES on the CUDA-core one (pa_run, pa_run_options,
+   * pa_run_static_workspace); cascade plans with a prefix and prefill plans
+   * refuse them with PA_ERR_UNSUPPORTED.  A scale for each block of tokens and
+   * kv head instead of one per tensor: pa_attention_options. */
   pa_dtype kv_dtype;
   float k_scale, v_scale;
   /* Rotary positions on the fly (README usage example: decode with
@@ -134,7 +140,7 @@ typedef struct {
    * in the cache) and the key of token t to position t; element pairs
    * (d, d + 64) turn by the angle pos * rope_theta^(-2d/128) (rotate-half
    * pairing; values are not rotated).  0 = no rotation.  Decode only, on the
-   * CUDA-core kernel, as for 8-bit caches. */
+   * CUDA-core kernel. */
   float rope_theta;
 } pa_problem;
 
