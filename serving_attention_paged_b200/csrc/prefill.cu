@@ -58,9 +58,10 @@
 // its o rows in a 16 KB region of its own, 64 columns at a time.
 // Options (kExt; pa_prefill_run_options): the softmax warps turn the raw scores
 // into final base-2 scores relative to the row's reference as they are read,
-// so that the exponentials need no further operation.  The kernel is then
-// bound by the FMA pipe (a packed FMA takes two of its cycles), so operations
-// per score are what counts: the bias is one FMA; a cap is cap * tanh as x
+// so that the exponentials need no further operation.  That lengthens each
+// half's chain (S, softmax, P V), which bounds the kernel, and a packed FMA takes
+// two cycles of its pipe, so operations per score are what counts: the bias is
+// one FMA; a cap is cap * tanh as x
 // times a polynomial in x^2 with every factor folded into its coefficients
 // (5 operations, bias added by the last) while the warp's scores are below half
 // the cap, a longer polynomial up to the cap, two MUFU operations per score in
@@ -72,7 +73,8 @@
 // options.  (Without a bias ascending order is the better one: its first tile
 // shows every row 128 keys, the diagonal tile as few as one.)  A half whose
 // rows see no key of the last tile then runs it fully masked, which keeps the
-// two halves' tiles aligned.
+// two halves' tiles aligned.  Measured for 8 x 1,024 appended tokens (fp16,
+// group 4, 206 GFLOP): cap and bias 306 us, cap 293, bias 251, neither 228.
 // Every mbarrier wait is bounded; on a timeout the kernel records it in the
 // workspace status word and unwinds instead of hanging.  Every parity wait
 // targets a barrier whose previous phase the waiting thread has itself

@@ -325,11 +325,15 @@ class PagedKV:
             ks = vs = row
             out_pages = k.shape[0]
         else:
+            ks = vs = row
             if k is None:
-                k = torch.empty(self._row_shape, dtype=_TORCH_DTYPES[self.dtype], device=self.device)
+                k = torch.empty(self._row_shape, dtype=self._row_dtype, device=self.device)
+            else:
+                ks = self._row_stride(k)
             if v is None:
-                v = torch.empty(self._row_shape, dtype=_TORCH_DTYPES[self.dtype], device=self.device)
-            ks, vs = self._row_stride(k), self._row_stride(v)
+                v = torch.empty(self._row_shape, dtype=self._row_dtype, device=self.device)
+            else:
+                vs = self._row_stride(v)
         with _on(self._dev):
             C.pa_kv_read(self.plan, k_pool, v_pool, k_scales, v_scales, kv_indices, k, ks, v, vs,
                          out_indices, out_pages, self.workspace, self.workspace_size, stream)
