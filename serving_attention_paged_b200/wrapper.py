@@ -9,8 +9,6 @@ kernels.
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import pagedattn as C
@@ -44,12 +42,15 @@ def _check_scales(k_scales, v_scales, blocks, num_kv_heads, dev):
                              f"cuda:{dev}")
 
 
-def _on(dev):
-    """Makes device ``dev`` current for a launch (nothing to do if it is)."""
-    return _HERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
-
-
-_HERE = contextlib.nullcontext()
+def _launch(dev, stream, call, *args):
+    """``call(*args, stream)`` with device ``dev`` current, on ``stream`` or
+    that device's current stream."""
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _launch(dev, stream, call, *args)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    return call(*args, stream)
 
 
 def _attention_options(problem, dev, k_pool, k_scales, v_scales, scale_block, logit_cap,
@@ -145,9 +146,8 @@ class PagedDecode:
             C.pa_cascade_run(self.plan, q, k_pool, v_pool, prefix_indices, kv_indices, o, lse,
                              self.workspace, self.workspace.numel(), stream)
         elif options is not None:
-            with _on(self._dev):
-                C.pa_run_options(self.plan, options, q, k_pool, v_pool, kv_indices, o, lse,
-                                 self.workspace, self.workspace.numel(), stream)
+            _launch(self._dev, stream, C.pa_run_options, self.plan, options, q, k_pool, v_pool,
+                    kv_indices, o, lse, self.workspace, self.workspace.numel())
         else:
             C.pa_run(self.plan, q, k_pool, v_pool, kv_indices, o, lse, self.workspace,
                      self.workspace.numel(), stream)
@@ -207,9 +207,8 @@ class PagedPrefill:
             lse = torch.empty(self.total_q, self.num_qo_heads, dtype=torch.float32,
                               device=self.device)
         if options is not None:
-            with _on(self._dev):
-                C.pa_prefill_run_options(self.plan, options, q, k_pool, v_pool, kv_indices, o,
-                                         lse, self.workspace, self.workspace.numel(), stream)
+            _launch(self._dev, stream, C.pa_prefill_run_options, self.plan, options, q, k_pool,
+                    v_pool, kv_indices, o, lse, self.workspace, self.workspace.numel())
         else:
             C.pa_prefill_run(self.plan, q, k_pool, v_pool, kv_indices, o, lse, self.workspace,
                              self.workspace.numel(), stream)
@@ -259,11 +258,11 @@ class PagedKV:
         self._pool_elements = num_pages * page_size * num_kv_heads * head_dim
         self._scale_blocks = num_pages * page_size // self.scale_block
         self.workspace_bytes = C.pa_plan_workspace_bytes(self.plan)
-        with _on(self._dev):
-            self.workspace = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8,
-                                         device=self.device)
-            self.workspace_size = self.workspace.numel()
-            C.pa_plan_upload(self.plan, self.workspace, self.workspace_size, stream)
+        self.workspace = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8,
+                                     device=self.device)
+        self.workspace_size = self.workspace.numel()
+        _launch(self._dev, stream, C.pa_plan_upload, self.plan, self.workspace,
+                self.workspace_size)
 
     def _check_cache(self, k_pool, v_pool, k_scales, v_scales, kv_indices):
         dev, code, n = self._dev, self._code_dtype, self._pool_elements
@@ -300,9 +299,8 @@ class PagedKV:
         scales, in place."""
         self._check_cache(k_pool, v_pool, k_scales, v_scales, kv_indices)
         ks, vs = self._row_stride(k), self._row_stride(v)
-        with _on(self._dev):
-            C.pa_kv_append(self.plan, k, ks, v, vs, k_pool, v_pool, k_scales, v_scales,
-                           kv_indices, self.workspace, self.workspace_size, stream)
+        _launch(self._dev, stream, C.pa_kv_append, self.plan, k, ks, v, vs, k_pool, v_pool,
+                k_scales, v_scales, kv_indices, self.workspace, self.workspace_size)
 
     def read(self, k_pool, v_pool, k_scales, v_scales, kv_indices, k=None, v=None,
              out_indices=None, stream=None):
@@ -334,11 +332,10 @@ class PagedKV:
                 v = torch.empty(self._row_shape, dtype=self._row_dtype, device=self.device)
             else:
                 vs = self._row_stride(v)
-        with _on(self._dev):
-            C.pa_kv_read(self.plan, k_pool, v_pool, k_scales, v_scales, kv_indices, k, ks, v, vs,
-                         out_indices, out_pages, self.workspace, self.workspace_size, stream)
+        _launch(self._dev, stream, C.pa_kv_read, self.plan, k_pool, v_pool, k_scales, v_scales,
+                kv_indices, k, ks, v, vs, out_indices, out_pages, self.workspace,
+                self.workspace_size)
         return k, v
 
     def check(self, stream=None) -> int:
-        with _on(self._dev):
-            return C.pa_plan_check(self.plan, self.workspace, stream)
+        return _launch(self._dev, stream, C.pa_plan_check, self.plan, self.workspace)
