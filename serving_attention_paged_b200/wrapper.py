@@ -53,6 +53,17 @@ def _launch(dev, stream, call, *args):
     return call(*args, stream)
 
 
+def _empty(dev, stream, *size, dtype):
+    """``torch.empty`` on device ``dev`` for ``stream``'s use: a block that the
+    current stream has freed may still be in use there."""
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=dtype, device=dev)
+
+
 def _attention_options(problem, dev, k_pool, k_scales, v_scales, scale_block, logit_cap,
                        alibi_slopes):
     """The run's ``pa_attention_options``, or None if nothing is asked for."""
@@ -117,9 +128,10 @@ class PagedDecode:
         else:
             self.plan = C.pa_plan_create(self.problem, kv_indptr, last_page_len)
         self.workspace_bytes = C.pa_plan_workspace_bytes(self.plan)
-        self.workspace = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8,
-                                     device=self.device)
-        C.pa_plan_upload(self.plan, self.workspace, self.workspace.numel(), stream)
+        self.workspace = _empty(self.device, stream, max(self.workspace_bytes, 256),
+                                dtype=torch.uint8)
+        _launch(self._dev, stream, C.pa_plan_upload, self.plan, self.workspace,
+                self.workspace.numel())
 
     def work_items(self):
         return C.pa_plan_work_items(self.plan)
@@ -137,11 +149,11 @@ class PagedDecode:
                                      scale_block, logit_cap, alibi_slopes)
         _require(options is None or not self.prefix_len, "a cascade run takes no options")
         if o is None:
-            o = torch.empty(self.batch, self.num_qo_heads, self.head_dim,
-                            dtype=_TORCH_DTYPES[self.dtype], device=self.device)
+            o = _empty(self.device, stream, self.batch, self.num_qo_heads, self.head_dim,
+                       dtype=_TORCH_DTYPES[self.dtype])
         if lse is None:
-            lse = torch.empty(self.batch, self.num_qo_heads, dtype=torch.float32,
-                              device=self.device)
+            lse = _empty(self.device, stream, self.batch, self.num_qo_heads,
+                         dtype=torch.float32)
         if self.prefix_len:
             C.pa_cascade_run(self.plan, q, k_pool, v_pool, prefix_indices, kv_indices, o, lse,
                              self.workspace, self.workspace.numel(), stream)
@@ -154,7 +166,7 @@ class PagedDecode:
         return o, lse
 
     def check(self, stream=None) -> int:
-        return C.pa_plan_check(self.plan, self.workspace, stream)
+        return _launch(self._dev, stream, C.pa_plan_check, self.plan, self.workspace)
 
 
 class PagedPrefill:
@@ -184,9 +196,10 @@ class PagedPrefill:
         self.plan = C.pa_prefill_plan_create(self.problem, causal, qo_indptr, kv_indptr,
                                              last_page_len)
         self.workspace_bytes = C.pa_plan_workspace_bytes(self.plan)
-        self.workspace = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8,
-                                     device=self.device)
-        C.pa_plan_upload(self.plan, self.workspace, self.workspace.numel(), stream)
+        self.workspace = _empty(self.device, stream, max(self.workspace_bytes, 256),
+                                dtype=torch.uint8)
+        _launch(self._dev, stream, C.pa_plan_upload, self.plan, self.workspace,
+                self.workspace.numel())
 
     def tiles(self):
         return C.pa_plan_prefill_tiles(self.plan)
@@ -201,11 +214,11 @@ class PagedPrefill:
         options = _attention_options(self.problem, self._dev, k_pool, None, None, None,
                                      logit_cap, alibi_slopes)
         if o is None:
-            o = torch.empty(self.total_q, self.num_qo_heads, self.head_dim,
-                            dtype=_TORCH_DTYPES[self.dtype], device=self.device)
+            o = _empty(self.device, stream, self.total_q, self.num_qo_heads, self.head_dim,
+                       dtype=_TORCH_DTYPES[self.dtype])
         if lse is None:
-            lse = torch.empty(self.total_q, self.num_qo_heads, dtype=torch.float32,
-                              device=self.device)
+            lse = _empty(self.device, stream, self.total_q, self.num_qo_heads,
+                         dtype=torch.float32)
         if options is not None:
             _launch(self._dev, stream, C.pa_prefill_run_options, self.plan, options, q, k_pool,
                     v_pool, kv_indices, o, lse, self.workspace, self.workspace.numel())
@@ -215,7 +228,7 @@ class PagedPrefill:
         return o, lse
 
     def check(self, stream=None) -> int:
-        return C.pa_plan_check(self.plan, self.workspace, stream)
+        return _launch(self._dev, stream, C.pa_plan_check, self.plan, self.workspace)
 
 
 class PagedKV:
@@ -258,8 +271,8 @@ class PagedKV:
         self._pool_elements = num_pages * page_size * num_kv_heads * head_dim
         self._scale_blocks = num_pages * page_size // self.scale_block
         self.workspace_bytes = C.pa_plan_workspace_bytes(self.plan)
-        self.workspace = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8,
-                                     device=self.device)
+        self.workspace = _empty(self.device, stream, max(self.workspace_bytes, 256),
+                                dtype=torch.uint8)
         self.workspace_size = self.workspace.numel()
         _launch(self._dev, stream, C.pa_plan_upload, self.plan, self.workspace,
                 self.workspace_size)
@@ -325,11 +338,11 @@ class PagedKV:
         else:
             ks = vs = row
             if k is None:
-                k = torch.empty(self._row_shape, dtype=self._row_dtype, device=self.device)
+                k = _empty(self.device, stream, *self._row_shape, dtype=self._row_dtype)
             else:
                 ks = self._row_stride(k)
             if v is None:
-                v = torch.empty(self._row_shape, dtype=self._row_dtype, device=self.device)
+                v = _empty(self.device, stream, *self._row_shape, dtype=self._row_dtype)
             else:
                 vs = self._row_stride(v)
         _launch(self._dev, stream, C.pa_kv_read, self.plan, k_pool, v_pool, k_scales, v_scales,

@@ -488,6 +488,27 @@ def test_options_on_another_stream():
     _close((to_np(o2), to_np(lse2)), ref, "f16", "current stream")
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_allocated_for_the_given_stream(handle):
+    """Outputs that run makes for another stream (a Stream, or its handle) are
+    no blocks on which the current stream's earlier work is still to come."""
+    c = Case([300, 41], 4, 16, "f16", "e4m3", 8, seed=26)
+    pd = c.plan()
+    dev = [c.q.cuda(), *[p.cuda() for p in c.pools], torch.from_numpy(c.w.kv_indices).cuda()]
+    kw = dict(k_scales=c.k_scales.cuda(), v_scales=c.v_scales.cuda(), scale_block=8)
+    want = pd.run(*dev, **kw)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed = [torch.empty_like(w) for w in want]
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    for f in freed:
+        f.fill_(7.0)
+    del f, freed
+    got = pd.run(*dev, stream=s.cuda_stream if handle else s, **kw)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
 @pytest.mark.parametrize("kernel", ["cuda_cores", "tensor_cores"])
 @pytest.mark.parametrize("fmt", [None, "e4m3"])
 def test_distances_past_2_to_24(fmt, kernel):

@@ -399,3 +399,23 @@ def test_single_head_rows_at_any_inner_stride():
         a.copy_(b)
     c.plan().append(*x, *dev)
     _check_append(c, dev)
+
+
+def test_read_allocates_for_the_given_stream():
+    """Outputs that read makes for another stream are no blocks on which the
+    current stream's earlier work is still to come."""
+    c = Cache([40, 17], [40, 17], 16, 16, "f16", "e4m3", seed=43)
+    dev = c.device()
+    pk = c.plan()
+    pk.append(c.x[0].cuda(), c.x[1].cuda(), *dev)
+    want = pk.read(*dev)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed = [torch.empty_like(w) for w in want]
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    for f in freed:
+        f.fill_(7.0)
+    del f, freed
+    got = pk.read(*dev, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
