@@ -381,9 +381,10 @@ pa_status pa_kv_plan_create(const pa_problem* problem, int32_t scale_block,
  *   codes of N = x / scale, rounded to nearest even, saturating (infinities
  *           too); NaN stays NaN.
  * Nothing else of the pools and scales is written, rows of the block past the
- * request's last token included.  A block that receives tokens may belong to
- * one request only (two requests appending into one block race), and no other
- * work may read or write it meanwhile.  One launch, no synchronisation. */
+ * request's last token included.  A page that receives tokens may stand in the
+ * tables once only (two requests appending into one block race, and so do two
+ * places of one request's table), and no other work may read or write its
+ * blocks meanwhile.  One launch, no synchronisation. */
 pa_status pa_kv_append(pa_plan_t plan, const void* k, int64_t k_stride, const void* v,
                        int64_t v_stride, void* k_pool, void* v_pool, float* k_scales,
                        float* v_scales, const int32_t* d_kv_indices, void* d_workspace,
@@ -395,7 +396,8 @@ pa_status pa_kv_append(pa_plan_t plan, const void* k, int64_t k_stride, const vo
  * and page j of request b goes to page d_out_indices[kv_indptr[b] + j] (the
  * strides are then num_kv_heads * 128): a prefill plan of the same tables
  * reads them with d_out_indices as its kv_indices.  Rows of tokens that are
- * not the plan's are left as they were.  Under PA_FLAG_CHECK_INDICES both
+ * not the plan's are left as they were.  Of places that name one page of
+ * d_out_indices any may be the one it holds afterwards.  Under PA_FLAG_CHECK_INDICES both
  * index arrays are bounds-checked; tokens on a bad page are skipped. */
 pa_status pa_kv_read(pa_plan_t plan, const void* k_pool, const void* v_pool,
                      const float* k_scales, const float* v_scales, const int32_t* d_kv_indices,

@@ -53,15 +53,17 @@ def _launch(dev, stream, call, *args):
     return call(*args, stream)
 
 
-def _empty(dev, stream, *size, dtype):
-    """``torch.empty`` on device ``dev`` for ``stream``'s use: a block that the
-    current stream has freed may still be in use there."""
+def _empty(stream):
+    """``torch.empty`` for ``stream``'s use (None: the current one's): a block
+    that the current stream has freed may still be in use there."""
     if stream is None:
-        return torch.empty(size, dtype=dtype, device=dev)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(size, dtype=dtype, device=dev)
+        return torch.empty
+
+    def empty(*size, dtype, device):
+        on = torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream
+        with torch.cuda.stream(on):
+            return torch.empty(*size, dtype=dtype, device=device)
+    return empty
 
 
 def _attention_options(problem, dev, k_pool, k_scales, v_scales, scale_block, logit_cap,
@@ -128,8 +130,8 @@ class PagedDecode:
         else:
             self.plan = C.pa_plan_create(self.problem, kv_indptr, last_page_len)
         self.workspace_bytes = C.pa_plan_workspace_bytes(self.plan)
-        self.workspace = _empty(self.device, stream, max(self.workspace_bytes, 256),
-                                dtype=torch.uint8)
+        self.workspace = _empty(stream)(max(self.workspace_bytes, 256), dtype=torch.uint8,
+                                        device=self.device)
         _launch(self._dev, stream, C.pa_plan_upload, self.plan, self.workspace,
                 self.workspace.numel())
 
@@ -148,12 +150,12 @@ class PagedDecode:
         options = _attention_options(self.problem, self._dev, k_pool, k_scales, v_scales,
                                      scale_block, logit_cap, alibi_slopes)
         _require(options is None or not self.prefix_len, "a cascade run takes no options")
+        empty = _empty(stream)
         if o is None:
-            o = _empty(self.device, stream, self.batch, self.num_qo_heads, self.head_dim,
-                       dtype=_TORCH_DTYPES[self.dtype])
+            o = empty(self.batch, self.num_qo_heads, self.head_dim,
+                      dtype=_TORCH_DTYPES[self.dtype], device=self.device)
         if lse is None:
-            lse = _empty(self.device, stream, self.batch, self.num_qo_heads,
-                         dtype=torch.float32)
+            lse = empty(self.batch, self.num_qo_heads, dtype=torch.float32, device=self.device)
         if self.prefix_len:
             C.pa_cascade_run(self.plan, q, k_pool, v_pool, prefix_indices, kv_indices, o, lse,
                              self.workspace, self.workspace.numel(), stream)
@@ -196,8 +198,8 @@ class PagedPrefill:
         self.plan = C.pa_prefill_plan_create(self.problem, causal, qo_indptr, kv_indptr,
                                              last_page_len)
         self.workspace_bytes = C.pa_plan_workspace_bytes(self.plan)
-        self.workspace = _empty(self.device, stream, max(self.workspace_bytes, 256),
-                                dtype=torch.uint8)
+        self.workspace = _empty(stream)(max(self.workspace_bytes, 256), dtype=torch.uint8,
+                                        device=self.device)
         _launch(self._dev, stream, C.pa_plan_upload, self.plan, self.workspace,
                 self.workspace.numel())
 
@@ -213,12 +215,12 @@ class PagedPrefill:
         need the causal mask."""
         options = _attention_options(self.problem, self._dev, k_pool, None, None, None,
                                      logit_cap, alibi_slopes)
+        empty = _empty(stream)
         if o is None:
-            o = _empty(self.device, stream, self.total_q, self.num_qo_heads, self.head_dim,
-                       dtype=_TORCH_DTYPES[self.dtype])
+            o = empty(self.total_q, self.num_qo_heads, self.head_dim,
+                      dtype=_TORCH_DTYPES[self.dtype], device=self.device)
         if lse is None:
-            lse = _empty(self.device, stream, self.total_q, self.num_qo_heads,
-                         dtype=torch.float32)
+            lse = empty(self.total_q, self.num_qo_heads, dtype=torch.float32, device=self.device)
         if options is not None:
             _launch(self._dev, stream, C.pa_prefill_run_options, self.plan, options, q, k_pool,
                     v_pool, kv_indices, o, lse, self.workspace, self.workspace.numel())
@@ -271,8 +273,8 @@ class PagedKV:
         self._pool_elements = num_pages * page_size * num_kv_heads * head_dim
         self._scale_blocks = num_pages * page_size // self.scale_block
         self.workspace_bytes = C.pa_plan_workspace_bytes(self.plan)
-        self.workspace = _empty(self.device, stream, max(self.workspace_bytes, 256),
-                                dtype=torch.uint8)
+        self.workspace = _empty(stream)(max(self.workspace_bytes, 256), dtype=torch.uint8,
+                                        device=self.device)
         self.workspace_size = self.workspace.numel()
         _launch(self._dev, stream, C.pa_plan_upload, self.plan, self.workspace,
                 self.workspace_size)
@@ -309,7 +311,8 @@ class PagedKV:
     def append(self, k, v, k_pool, v_pool, k_scales, v_scales, kv_indices, stream=None):
         """Quantise the plan's tokens (``k``, ``v``: ``[total_q, num_kv_heads,
         128]``, rows at any stride that is a multiple of 8) into the pools and
-        scales, in place."""
+        scales, in place.  A page that receives tokens stands in the tables
+        once only."""
         self._check_cache(k_pool, v_pool, k_scales, v_scales, kv_indices)
         ks, vs = self._row_stride(k), self._row_stride(v)
         _launch(self._dev, stream, C.pa_kv_append, self.plan, k, ks, v, vs, k_pool, v_pool,
@@ -337,12 +340,13 @@ class PagedKV:
             out_pages = k.shape[0]
         else:
             ks = vs = row
+            empty = _empty(stream)
             if k is None:
-                k = _empty(self.device, stream, *self._row_shape, dtype=self._row_dtype)
+                k = empty(self._row_shape, dtype=self._row_dtype, device=self.device)
             else:
                 ks = self._row_stride(k)
             if v is None:
-                v = _empty(self.device, stream, *self._row_shape, dtype=self._row_dtype)
+                v = empty(self._row_shape, dtype=self._row_dtype, device=self.device)
             else:
                 vs = self._row_stride(v)
         _launch(self._dev, stream, C.pa_kv_read, self.plan, k_pool, v_pool, k_scales, v_scales,
