@@ -381,10 +381,10 @@ pa_status pa_kv_plan_create(const pa_problem* problem, int32_t scale_block,
  *   codes of N = x / scale, rounded to nearest even, saturating (infinities
  *           too); NaN stays NaN.
  * Nothing else of the pools and scales is written, rows of the block past the
- * request's last token included.  A page that receives tokens may stand in the
- * tables once only (two requests appending into one block race, and so do two
- * places of one request's table), and no other work may read or write its
- * blocks meanwhile.  One launch, no synchronisation. */
+ * request's last token included.  A block may receive tokens
+ * through one place of the tables only (two requests appending into one block
+ * race, and so do two places of one request's table), and no other work may
+ * read or write it meanwhile.  One launch, no synchronisation. */
 pa_status pa_kv_append(pa_plan_t plan, const void* k, int64_t k_stride, const void* v,
                        int64_t v_stride, void* k_pool, void* v_pool, float* k_scales,
                        float* v_scales, const int32_t* d_kv_indices, void* d_workspace,

@@ -311,8 +311,8 @@ class PagedKV:
     def append(self, k, v, k_pool, v_pool, k_scales, v_scales, kv_indices, stream=None):
         """Quantise the plan's tokens (``k``, ``v``: ``[total_q, num_kv_heads,
         128]``, rows at any stride that is a multiple of 8) into the pools and
-        scales, in place.  A page that receives tokens stands in the tables
-        once only."""
+        scales, in place.  A block receives tokens through one place of the
+        tables only."""
         self._check_cache(k_pool, v_pool, k_scales, v_scales, kv_indices)
         ks, vs = self._row_stride(k), self._row_stride(v)
         _launch(self._dev, stream, C.pa_kv_append, self.plan, k, ks, v, vs, k_pool, v_pool,
