@@ -320,6 +320,17 @@ pa_status pa_prefill_run(pa_plan_t plan, const void* q, const void* k_pool, cons
  * pa_problem.k_scale / v_scale, which must be 1.  Scales are 0 or of
  * magnitude 2^-60 to 2^60 (what pa_kv_append writes).
  *
+ * How exact a token's weight is.  The CUDA-core kernel (PA_FLAG_CUDA_CORES)
+ * holds each in fp32.  The tensor-core kernel, over 8-bit pools, works with
+ * p |v_scale|, as a number of 15 bits that goes down to 2^-25 of the largest
+ * of the CTA's tokens of the request; what is dropped below that is carried
+ * on, so that many small weights (a long tail behind an attention sink) keep
+ * their sum to 2^-18 of that largest weight, whatever the length.  Where V
+ * scales differ by more than 2^20 between blocks of like weight, elements in
+ * which the large blocks' codes are 0 lose the precision of the small ones.
+ * Both kernels sum in fp32, in which equal weights below 2^-24 of the largest
+ * can vanish beside it.
+ *
  * Scores: with s = sm_scale <q, k> (and the positions' rotation, if any),
  *   s <- logit_cap * tanh(s / logit_cap)     if logit_cap > 0, then
  *   s <- s - alibi_slopes[hq] * distance     if alibi_slopes (device, fp32 [Hq]),

@@ -315,19 +315,30 @@ __device__ __forceinline__ __half2 e4m3x2_value(uint16_t c) {
   return *reinterpret_cast<__half2*>(&d);
 }
 
-// Two P values (below 448) as n E4M3 terms p ~ t0 + t1/16 + t2/256 (+
-// t3/4096): t0 = e4m3(p); the residual (p - t0) * 16 is exact in fp32 and
-// rounded to fp16 (11 more bits, ~15 in all); t1.. take it apart, exactly for n = 4.
-template <int n>
-__device__ __forceinline__ void split_p(float lo, float hi, uint16_t (&t)[n]) {
+// Two P values (below 448) as four E4M3 terms p ~ t0 + t1/16 + t2/256 +
+// t3/4096: t0 = e4m3(p); the residual (p - t0) * 16 is exact in fp32 and
+// rounded to fp16 (11 more bits, ~15 in all); t1..t3 take it apart, exactly
+// but below E4M3's smallest step, 2^-9 of t3 or 2^-21 of p.  What a small
+// weight loses there may be half of it or all, and equal weights all lose the
+// same: with kCarry it goes to the same thread's next weight of the head
+// instead (in units of 2^-12, at most the half step 2^-10; of a large weight,
+// whose residual is a 2^-15 part of it, no more than that either).  A weight
+// of 0 stays 0: a carry alone is no more than half a step and rounds to 0.
+template <bool kCarry>
+__device__ __forceinline__ void split_p(float lo, float hi, uint16_t (&t)[4], __half2& carry) {
   t[0] = e4m3x2(lo, hi);
   const float2 v = __half22float2(e4m3x2_value(t[0]));
   __half2 r = __floats2half2_rn((lo - v.x) * 16.f, (hi - v.y) * 16.f);
   const __half2 k16 = __float2half2_rn(16.f);
 #pragma unroll
-  for (int k = 1; k < n; ++k) {
+  for (int k = 1; k < 4; ++k) {
+    if (kCarry && k == 3) r = __hadd2(r, carry);
     t[k] = e4m3x2(r);
-    if (k < n - 1) r = __hmul2(__hsub2(r, e4m3x2_value(t[k])), k16);
+    if (k < 3) r = __hmul2(__hsub2(r, e4m3x2_value(t[k])), k16);
+  }
+  if constexpr (kCarry) {
+    const __half2 most = __float2half2_rn(0x1p-10f);
+    carry = __hmax2(__hmin2(__hsub2(r, e4m3x2_value(t[3])), most), __hneg2(most));
   }
 }
 
@@ -398,15 +409,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
   // rounding of P, and a lone 11-bit P would leave o up to 2^-11 |v| off them.
   constexpr bool kSplit = !k8 && (Fmt<Tag>::v == 1 || kExt);
   // 8-bit pools: E4M3 terms of q (kQT) and of P (kPT) per head.
-  // With options a softmax thread has more to do per score, and P takes three:
-  // 12 significant bits (an fp16 P's 11 and one more).  The reference is set
-  // 2^kHead below the maximum, so that the smallest step, 2^-17 of the reference,
-  // is 2^-21 of the largest weight as with four terms (many tokens far below it,
-  // as behind an attention sink, still count), and moves when a weight would
-  // pass 2^8.7 (E4M3 holds 448).  A larger kHead would move it too often: with
-  // 7, a factor of 2 over the first maximum is enough, and each move waits for
-  // the P V in flight (tile period 4,460 cycles for 3,165 at group 8).
-  constexpr int kQT = Fmt<Tag>::v == 1 ? 2 : 3, kPT = kExt ? 3 : 4;
+  // With options the reference is set 2^kHead below the maximum, so that the
+  // terms' smallest step, 2^-21 of the reference, is 2^-25 of the largest
+  // weight or less, and it moves when a weight would pass 2^8.7 (E4M3 holds
+  // 448); what falls below that step is carried from tile to tile (split_p),
+  // so the many small weights of a long request add up whatever their size.
+  // A larger kHead would move the reference too often: with 7, a factor of 2
+  // over the first maximum is enough, and each move waits for the P V in
+  // flight (tile period 4,460 cycles for 3,165 at group 8).
+  constexpr int kQT = Fmt<Tag>::v == 1 ? 2 : 3, kPT = 4;
   constexpr float kHead = k8 && kExt ? 4.f : 0.f;
   constexpr float kMove = k8 && kExt ? 8.7f : kSlack;
   // columns of one S^T / O^T buffer (the MMA N)
@@ -857,6 +868,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
           slope2[hh] = a.score.slopes ? __ldg(a.score.slopes + it.kv_head * G + hh) * kLog2e : 0.f;
       }
       float m[G], lsum[G], scl[G];
+      [[maybe_unused]] __half2 carry[kHalves][(G + 1) / 2];  // options of 8-bit pools: split_p's
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int k = 0; k < (G + 1) / 2; ++k) carry[h][k] = __float2half2_rn(0.f);
 #pragma unroll
       for (int hh = 0; hh < G; ++hh) {
         m[hh] = -INFINITY;
@@ -993,6 +1009,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
             r[cc] = __float_as_uint(__uint_as_float(r[cc]) * alpha[cc % G]);
           tmem_st<kColsLd>(oaddr, r);
           tc::tmem_wait_st();
+          if constexpr (k8 && kExt) {
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+              for (int hh = 0; hh < G; hh += 2)
+                carry[h][hh / 2] = __hmul2(
+                    carry[h][hh / 2], __floats2half2_rn(alpha[hh], alpha[hh + 1 < G ? hh + 1 : hh]));
+          }
         }
         // P^T(t) for this thread's token; the row sums add the rounded values
         if (t >= 2) {
@@ -1014,7 +1038,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
               ps += p[h][hh];
               if constexpr (kExt) p[h][hh] *= vs[h];  // the weight in P V
             }
-            // the MMA's weights agree with p to ~2^-15: the row sums take p
+            // the row sums take p itself: the MMA's weights agree with it to
+            // 2^-15, or to 2^-22 of the reference where that is more (with
+            // options the latter adds up to nothing, see split_p)
             lsum[hh] = fmaf(lsum[hh], alpha[hh], ps);
             m[hh] = mn[hh];
           }
@@ -1024,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
 #pragma unroll
             for (int hh = 0; hh < G; hh += 2) {
               uint16_t tm[kPT];
-              split_p<kPT>(p[h][hh], hh + 1 < G ? p[h][hh + 1] : 0.f, tm);
+              split_p<kExt>(p[h][hh], hh + 1 < G ? p[h][hh + 1] : 0.f, tm, carry[h][hh / 2]);
 #pragma unroll
               for (int k = 0; k < kPT; ++k) {
                 const int n = k * G + hh;
