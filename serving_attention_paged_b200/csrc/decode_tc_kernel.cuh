@@ -417,9 +417,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
   // A larger kHead would move the reference too often: with 7, a factor of 2
   // over the first maximum is enough, and each move waits for the P V in
   // flight (tile period 4,460 cycles for 3,165 at group 8).
+  // An fp16 P over 16-bit pools has steps of 2^-24 below 2^-14: its reference
+  // lies 2^7 below the maximum and moves at 2^15, as often as without, and the
+  // steps are 2^-31 of the largest weight.  A bf16 P has fp32's exponents.
   constexpr int kQT = Fmt<Tag>::v == 1 ? 2 : 3, kPT = 4;
-  constexpr float kHead = k8 && kExt ? 4.f : 0.f;
-  constexpr float kMove = k8 && kExt ? 8.7f : kSlack;
+  constexpr bool kHalfP = !k8 && Fmt<Tag>::v == 0;
+  constexpr float kHead = !kExt ? 0.f : k8 ? 4.f : kHalfP ? 7.f : 0.f;
+  constexpr float kMove = !kExt ? kSlack : k8 ? 8.7f : kHead + kSlack;
   // columns of one S^T / O^T buffer (the MMA N)
   constexpr int kNC = k8 ? (kPT * G <= 16 ? 16 : 32) : kN;
   // S^T columns a softmax thread reads, O^T columns the epilogue reads

@@ -79,6 +79,7 @@ def _decode(case, dtype, kernel, fmt, **kw):
 
 
 def _close(got, o, lse, dtype, what, lse_more=0.0):
+    assert np.isfinite(got[0]).all(), what
     o = np.broadcast_to(o, got[0].shape)
     off = got[1] - lse
     assert_close(got[0], lse + np.sign(off) * np.maximum(np.abs(off) - lse_more, 0), o,
@@ -146,3 +147,16 @@ def test_values_beside_a_block_of_far_larger_scale(kernel, spread):
     # bf16 rounds the output by up to 2^-8 of it
     assert np.all(np.abs(to_np(o) - ref) <= (2e-3 + 2.0 ** -8) * ref)
     assert np.abs(to_np(lse) - np.log(w.sum())).max() <= 1e-3
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("kernel", ["cuda_cores", "tensor_cores"])
+def test_tail_behind_a_sink_in_a_16bit_cache(kernel, dtype):
+    """Equal weights of 12.5 and 1.5 steps of 2^-24 of the largest: fp16's
+    subnormals."""
+    for pages, weight in ((128, 12.5 * 2.0 ** -24), (1024, 1.5 * 2.0 ** -24)):
+        case = Tail(pages, weight, 0.0)
+        o, lse = case.expected()
+        got = _decode(case, dtype, kernel, None, alibi_slopes=torch.zeros(G, device="cuda"))
+        sums = pages * P / (32 if kernel == "cuda_cores" else 128) * 2.0 ** -24
+        _close(got, o, lse, dtype, kernel, sums)
