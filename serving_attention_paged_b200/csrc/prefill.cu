@@ -135,7 +135,11 @@ constexpr int kBarQFull = 0, kBarQEmpty = kBarQFull + 2, kBarKFull = kBarQEmpty 
 constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 8 + 1024;  // + slack to align to 1 KB
 constexpr uint32_t kTmemCols = 512;
 constexpr float kSlack = 8.f;
-constexpr float kSumMax = 8192.f;  // options: a tile's sum of P that keeps the reference
+// options: the reference lies 2^kHead below the maximum, so that fp16 P's smallest
+// step (2^-24) is 2^-28 of the largest weight; a tile's sum of P up to kSumMax keeps
+// it.  At the maximum, a tail of 131,072 tokens behind an attention sink lost up to
+// 4 % of each weight, which the row sum (of p before its rounding) took whole.
+constexpr float kHead = 4.f, kSumMax = 32768.f;
 constexpr int kPolyPairsPer8 = 1;  // pairs of exponentials (of 8) on the FMA pipe
 constexpr float kLn2 = 0.6931471805599453f;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
@@ -668,14 +672,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           else run(OptionScores<false>(slope2, base));
           if (masked) mask();
           // Not late: P's sum bounds every p, so the reference stays while the sum
-          // does (p <= 2^13 is far inside fp16's and bf16's range) and the tile
+          // does (p <= 2^15 is inside fp16's and bf16's range) and the tile
           // maximum is not needed; its 64 maxima took 450 cycles of a tile's 3,550.
           bool moved = !late && !(psum <= kSumMax);
           float delta = 0.f;
           if (late || __any_sync(0xffffffffu, moved)) {
             const float tmax = tile_max();
-            if (late) moved = tmax > (fresh ? -INFINITY : kSlack);
-            if (moved) delta = fresh ? tmax : fmaxf(tmax, 0.f);
+            if (late) moved = tmax > (fresh ? -INFINITY : kHead + kSlack);
+            if (moved) delta = (fresh ? tmax : fmaxf(tmax, 0.f)) - kHead;
           }
           const bool any_moved = __any_sync(0xffffffffu, moved);
           if (moved) {
