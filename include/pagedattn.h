@@ -218,6 +218,10 @@ typedef struct {
  *   lse = ln sum_t exp(s_t) (fp32), o = sum_t exp(s_t - lse) v_pool[row(b, t), h, :]
  *   rounded once to the input type; a token that sees no key gets o = 0,
  *   lse = -inf.
+ * A value past a token's position weighs 0, and 0 x infinity is NaN: an
+ * infinity or NaN reaches the tokens that run in one half of a tile (128 / G
+ * tokens, see below) with a token whose last 128-key tile (keys 128 j to
+ * 128 j + 127 of the request) holds it, and no others.
  * Layouts: q and o are [total_q, num_qo_heads, head_dim] with total_q =
  * qo_indptr[batch]; lse is [total_q, num_qo_heads]; the pools as above.
  * Work: the query tokens of each request are cut into tiles of 256 / G

@@ -72,8 +72,9 @@
 // exponentials can be taken before the tile maximum is known, as without
 // options.  (Without a bias ascending order is the better one: its first tile
 // shows every row 128 keys, the diagonal tile as few as one.)  A half whose
-// rows see no key of the last tile then runs it fully masked, which keeps the
-// two halves' tiles aligned.  Measured for 8 x 1,024 appended tokens (fp16,
+// rows see no key of the last tile then runs its S and softmax fully masked,
+// which keeps the two halves' tiles aligned, but no P V: 0 x V would carry
+// an infinity or NaN among the tile's values into rows that do not see it.  Measured for 8 x 1,024 appended tokens (fp16,
 // group 4, 206 GFLOP): cap and bias 306 us, cap 293, bias 251, neither 228.
 // Every mbarrier wait is bounded; on a timeout the kernel records it in the
 // workspace status word and unwinds instead of hanging.  Every parity wait
@@ -195,9 +196,11 @@ __device__ __forceinline__ int ld_nc_volatile(const int32_t* p) {
 // rest; half 0's last token sees fewer keys, so it may need fewer tiles).
 struct Item {
   int h, q_begin, n_q, page_begin, kv_base, kv_end, nq0, nq1, nt0, nt1, ntiles;
+  bool unseen0;  // last to first: half 0 sees no key of its first tile
 };
 
-// Last to first (rev), both halves run all of the item's tiles.
+// Last to first (rev), both halves run all of the item's tiles.  Half 1 has at
+// most 128 tokens more than half 0, so at most one tile is beyond half 0.
 __device__ __forceinline__ Item load_item(const PrefillArgs& a, int j, bool rev) {
   Item it;
   const int w = __ldg(a.sched + j);
@@ -214,6 +217,7 @@ __device__ __forceinline__ Item load_item(const PrefillArgs& a, int j, bool rev)
   it.nt0 = (min(it.kv_base + it.nq0, it.kv_end) + kKeys - 1) / kKeys;
   it.nt1 = it.nq1 > 0 ? (it.kv_end + kKeys - 1) / kKeys : 0;
   it.ntiles = max(it.nt0, it.nt1);
+  it.unseen0 = rev && it.nt0 < it.ntiles;
   if (rev && it.nq1 > 0) it.nt0 = it.ntiles;
   return it;
 }
@@ -478,7 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!ok) break;
               ++pc[hf];
               tc::fence_after_sync();
-              if (tc::elect_one_sync()) issue_pv(hf, g % kVStages, v == 0);
+              const int first = hf == 0 && it.unseen0;  // the half's first P V
+              if (v >= first && tc::elect_one_sync()) issue_pv(hf, g % kVStages, v == first);
               __syncwarp();
             }
             if (kt == 0) ok = wait_all(kBarQFull + hf, jj & 1);
@@ -639,7 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kExt) {
           // x becomes the final score relative to the row's reference.  A row
           // without one yet (it saw no key so far) takes its first tile's maximum;
-          // its O and l are zero, so any factor will do.
+          // its O is zero or will be overwritten (unseen0) and its l is zero, so
+          // any factor will do.
           const bool fresh = m == -INFINITY;
           const bool late = masked || __any_sync(0xffffffffu, fresh);
           const float mref = fresh ? 0.f : m;

@@ -1,8 +1,11 @@
 """Prefill with options where its arithmetic is at its limits."""
+import numpy as np
 import pytest
 import torch
 
-from parity import to_np
+from oracle import cache
+from parity import assert_close, to_np
+from test_attention_options_gpu import Case
 from test_small_weights_gpu import D, G, HALF, P, Tail, _close
 
 pytestmark = pytest.mark.gpu
@@ -30,3 +33,34 @@ def test_tail_behind_a_sink(dtype, slopes):
     ref, ref_lse = case.expected()
     # (the first new token misses one of 131,072 tokens of the tail)
     _close((to_np(o), to_np(lse)), ref, ref_lse, dtype, str(slopes))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("group,kv,new", [(1, 128, 256), (1, 0, 129), (2, 64, 128), (4, 96, 64),
+                                          (4, 992, 64), (8, 112, 32)])
+def test_values_of_later_tiles_do_not_reach_earlier_tokens(group, kv, new, dtype):
+    """Infinities and NaN among the values of the last new tokens.  Tokens whose
+    128-key tiles end before them (those of an item's first half, here) must
+    not notice, with a distance bias as without."""
+    from serving_attention_paged_b200.wrapper import PagedPrefill
+    per_half = 128 // group
+    length = kv + new
+    c = Case([length], group, 8, dtype, seed=group + new, qo=[new])
+    w = c.w
+    rows = torch.from_numpy(cache._rows(0, w.kv_indptr, w.kv_indices, w.last_page_len, 8))
+    # tokens of the first half see keys below kv + per_half
+    edge = -(-(kv + per_half) // 128) * 128
+    assert edge < length, "the case has a tile that the first half does not see"
+    ref = c.expected(qo_indptr=w.qo_indptr, logit_cap=20.0, alibi_slopes=c.slopes)
+    plain = c.expected(qo_indptr=w.qo_indptr)
+    v = c.pools[1].view(-1, 2, D)
+    v[rows[edge:], :, ::2] = float("inf")
+    v[rows[edge:], :, 1::2] = float("nan")
+    pf = PagedPrefill(w.qo_indptr, w.kv_indptr, w.last_page_len, num_qo_heads=w.num_qo_heads,
+                      num_kv_heads=2, page_size=8, dtype=dtype, sm_scale=w.sm_scale,
+                      num_pages=w.num_pages)
+    n = min(per_half, new)
+    for cap, slopes, want in ((0.0, False, plain), (20.0, True, ref)):
+        o, lse = c.run(pf, cap, slopes)
+        assert np.isfinite(o[:n]).all(), f"slopes={slopes}"
+        assert_close(o[:n], lse[:n], want[0][:n], want[1][:n], dtype, f"slopes={slopes}")
