@@ -63,7 +63,7 @@
 // two cycles of its pipe, so operations per score are what counts: the bias is
 // one FMA; a cap is cap * tanh as x
 // times a polynomial in x^2 with every factor folded into its coefficients
-// (5 operations, bias added by the last) while the warp's scores are below half
+// (6 operations, bias added by the last) while the warp's scores are below half
 // the cap, a longer polynomial up to the cap, two MUFU operations per score in
 // the rare tile beyond; and all exponentials stay on the MUFU unit.  With a
 // distance bias the key tiles run last to first: the bias falls away from the
@@ -237,9 +237,9 @@ struct OptionScores {
   }
   __device__ __forceinline__ float2 small(const CapPoly& cap, int c, float2 v) const {
     const float2 u = __fmul2_rn(v, v);
-    float2 p = make_float2(cap.k[3], cap.k[3]);
+    float2 p = make_float2(cap.k[4], cap.k[4]);
 #pragma unroll
-    for (int i = 2; i >= 0; --i) p = __ffma2_rn(p, u, make_float2(cap.k[i], cap.k[i]));
+    for (int i = 3; i >= 0; --i) p = __ffma2_rn(p, u, make_float2(cap.k[i], cap.k[i]));
     return __ffma2_rn(v, p, bias(c));
   }
   // any |v|; which branch a tile takes is uniform in the warp

@@ -61,25 +61,27 @@ inline void set_score_args(const pa_attention_options& o, ScoreArgs* a, float* s
 
 // cap_out * tanh(score_scale * x) for raw scores |x| <= small, as x times a
 // polynomial in x^2 with the powers of score_scale and the cap folded in: a
-// minimax fit of tanh(y) / y, degree 3 in y^2 on |y| <= 1/2, relative error
-// 5.5e-7 (a score of 15 is 8e-6 off).  |x| <= mid: |score_scale * x| <= 1.
+// minimax fit of tanh(y) / y, degree 4 in y^2 on |y| <= 1/2, relative error
+// 1.3e-8, below fp32's rounding.  (Degree 3 is one operation less and 5.4e-7
+// off, all one way for small scores: 9e-4 of a score of 1,600.)  |x| <= mid:
+// |score_scale * x| <= 1.
 struct CapPoly {
-  float k[4], small, mid;
+  float k[5], small, mid;
 };
 inline CapPoly make_cap_poly(const ScoreArgs& a, float score_scale) {
-  constexpr double c[4] = {0.999999463558197, -0.33326318860054016, 0.13190296292304993,
-                           -0.04440222680568695};
+  constexpr double c[5] = {0.9999999868759589, -0.3333306944690451, 0.13324780408767786,
+                           -0.05298614099119273, 0.017135126142517644};
   CapPoly out{};
   const double s = score_scale;
   double f = double(a.cap_out) * s;
-  for (int i = 0; i < 4; ++i, f *= s * s) out.k[i] = float(c[i] * f);
+  for (int i = 0; i < 5; ++i, f *= s * s) out.k[i] = float(c[i] * f);
   const double r = s < 0 ? -s : s;
   double reach = kTanhSmall;
-  if (std::fabs(out.k[3]) < 0x1p-120f) {  // a huge cap: the last term leaves fp32's range, but
-    out.k[3] = 0.f;                       // up to 2^-5 of it it is below 1e-10 of the score
+  if (std::fabs(out.k[4]) < 0x1p-120f) {  // a huge cap: the last terms leave fp32's range, but
+    out.k[3] = out.k[4] = 0.f;            // up to 2^-5 of it they are below 1e-10 of the score
     reach = 0x1p-5;
   }
-  const bool finite = std::isfinite(out.k[0]) && std::isfinite(out.k[3]);
+  const bool finite = std::isfinite(out.k[0]) && std::isfinite(out.k[4]);
   out.small = finite && r > 0 ? float(reach / r) : -1.f;
   out.mid = r > 0 ? float(1.0 / r) : INFINITY;
   return out;

@@ -64,3 +64,31 @@ def test_values_of_later_tiles_do_not_reach_earlier_tokens(group, kv, new, dtype
         o, lse = c.run(pf, cap, slopes)
         assert np.isfinite(o[:n]).all(), f"slopes={slopes}"
         assert_close(o[:n], lse[:n], want[0][:n], want[1][:n], dtype, f"slopes={slopes}")
+
+
+def test_small_scores_under_a_cap_are_exact_to_fp32():
+    """One key per token: lse is the capped score itself.  cap = 2^15,
+    sm_scale = 1 and scores of 160 to 1,640 (up to a twentieth of the cap).
+    Rounded constants common to all: log2 e and ln 2 (their product is within
+    0.7 of 2^-24 of 1), the polynomial's first coefficient (1), so at most 1.7
+    parts of 2^-24; the roundings of each score's own (product, exponent,
+    log-sum, last product) are within 4, of either sign, and their mean over
+    512 scores within 1.  (2^-24 = 6e-8.)  So the mean error is below 3 * 2^-24."""
+    from serving_attention_paged_b200.wrapper import PagedPrefill
+    n, cap = 512, 2.0 ** 15
+    g = np.random.default_rng(5)
+    s = g.uniform(0.005, 0.05, n) * cap
+    for dtype in ("f16", "bf16"):
+        a = torch.from_numpy(np.sqrt(s)).to(HALF[dtype])
+        q = torch.zeros(n, 1, D, dtype=HALF[dtype])
+        q[:, 0, 3] = a
+        k = torch.zeros(n, 8, 1, D, dtype=HALF[dtype])
+        k[:, 0, 0, 3] = a
+        exact = cap * np.tanh(a.double().numpy() ** 2 / cap)
+        pf = PagedPrefill(np.arange(n + 1), np.arange(n + 1), np.ones(n, np.int32), num_qo_heads=1,
+                          num_kv_heads=1, page_size=8, dtype=dtype, sm_scale=1.0, num_pages=n)
+        _, lse = pf.run(q.cuda(), k.cuda(), torch.zeros_like(k).cuda(),
+                        torch.arange(n, dtype=torch.int32, device="cuda"), logit_cap=cap)
+        off = to_np(lse)[:, 0] / exact - 1.0
+        assert abs(off.mean()) <= 3 * 2.0 ** -24, dtype
+        assert np.abs(off).max() <= 8 * 2.0 ** -24, dtype
