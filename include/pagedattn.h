@@ -405,15 +405,22 @@ pa_status pa_kv_append(pa_plan_t plan, const void* k, int64_t k_stride, const vo
                        float* v_scales, const int32_t* d_kv_indices, void* d_workspace,
                        size_t workspace_bytes, void* stream);
 
-/* Read the plan's tokens back: scale * code, rounded once to `dtype`.  With
- * d_out_indices null, into rows of k and v as pa_kv_append takes them.  Else
- * into pages: k and v are [num_out_pages, page_size, num_kv_heads, 128] pools
+/* pa_kv_read without d_out_indices, as num_out_pages: rows of tokens on a bad
+ * page are written as zeros. */
+#define PA_KV_ZERO_BAD_ROWS (-1)
+
+/* Read the plan's tokens back: scale * code, formed in fp32 (exact for scales
+ * that are powers of two) and rounded to `dtype`.  With d_out_indices null,
+ * into rows of k and v as pa_kv_append takes them.  Else into pages: k and v are [num_out_pages, page_size, num_kv_heads, 128] pools
  * and page j of request b goes to page d_out_indices[kv_indptr[b] + j] (the
  * strides are then num_kv_heads * 128): a prefill plan of the same tables
  * reads them with d_out_indices as its kv_indices.  Rows of tokens that are
  * not the plan's are left as they were.  Of places that name one page of
  * d_out_indices any may be the one it holds afterwards.  Under PA_FLAG_CHECK_INDICES both
- * index arrays are bounds-checked; tokens on a bad page are skipped. */
+ * index arrays are bounds-checked.  Tokens on a bad page (out of range under
+ * that flag, or negative) are skipped: their rows are left as they were, or
+ * with d_out_indices null and num_out_pages = PA_KV_ZERO_BAD_ROWS written as
+ * zeros, which is what attention takes them for. */
 pa_status pa_kv_read(pa_plan_t plan, const void* k_pool, const void* v_pool,
                      const float* k_scales, const float* v_scales, const int32_t* d_kv_indices,
                      void* k, int64_t k_stride, void* v, int64_t v_stride,

@@ -61,6 +61,7 @@ struct KvArgs {
   uint32_t num_kv_heads;
   int32_t log2_page, log2_block;
   bool check;
+  bool zero_bad;  // reads into rows: zeros for tokens on a bad page, which are else left alone
 };
 
 template <typename F> struct Format;
@@ -412,7 +413,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvArgs a) {
   for (int i = 0; i < kSteps; ++i) {
     const uint32_t r = __shfl_sync(0xffffffffu, rows, 2 * i + half);
     const uint32_t ro = __shfl_sync(0xffffffffu, out_rows, 2 * i + half);
-    if (r == kNoRow) continue;
+    const int t = t0 + 2 * i + half;
+    if (r == kNoRow && !(a.zero_bad && t >= begin && t < end)) continue;  // bad page: 0 * 0
     float y[8];
     from_fp8x8<F>(x[i], y);
     uint32_t w[4];
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvArgs a) {
     for (int e = 0; e < 4; ++e) w[e] = pack16(Tag{}, s[i] * y[2 * e], s[i] * y[2 * e + 1]);
     const int64_t out = a.out_indices
                             ? int64_t(ro) * a.num_kv_heads * D
-                            : (sp.row + int64_t(t0 + 2 * i + half - sp.begin)) * a.stride[kv];
+                            : (sp.row + int64_t(t - sp.begin)) * a.stride[kv];
     *reinterpret_cast<uint4*>(a.x[kv] + out + h * D + c * 8) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
@@ -482,6 +484,7 @@ int launch_kv_append(const pa_plan_s& plan, const KvPointers& p, void* stream) {
 int launch_kv_read(const pa_plan_s& plan, const KvPointers& p, void* stream) {
   KvArgs a = make_args(plan, p);
   if (a.n_units == 0) return 0;
+  a.zero_bad = !p.out_indices && p.num_out_pages == PA_KV_ZERO_BAD_ROWS;
   if (a.log2_block > 4) a.n_units <<= a.log2_block - 4;  // 16-token pieces of a span
   const unsigned ctas = (a.n_units + kWarps - 1) / kWarps;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

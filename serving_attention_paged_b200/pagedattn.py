@@ -28,6 +28,7 @@ PA_F16, PA_BF16, PA_F32, PA_E4M3, PA_E5M2 = 0, 1, 2, 3, 4
 PA_FLAG_CHECK_INDICES = 1
 PA_FLAG_CUDA_CORES = 2
 PA_FLAG_TENSOR_CORES = 4
+PA_KV_ZERO_BAD_ROWS = -1
 DTYPE_CODES = {"f16": PA_F16, "bf16": PA_BF16, "f32": PA_F32, "e4m3": PA_E4M3,
                "e5m2": PA_E5M2}
 

@@ -53,16 +53,17 @@ def _launch(dev, stream, call, *args):
     return call(*args, stream)
 
 
-def _empty(stream):
-    """``torch.empty`` for ``stream``'s use (None: the current one's): a block
-    that the current stream has freed may still be in use there."""
+def _empty(stream, make=torch.empty):
+    """``torch.empty`` (or ``make``) for ``stream``'s use (None: the current
+    one's): a block that the current stream has freed may still be in use
+    there."""
     if stream is None:
-        return torch.empty
+        return make
 
     def empty(*size, dtype, device):
         on = torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream
         with torch.cuda.stream(on):
-            return torch.empty(*size, dtype=dtype, device=device)
+            return make(*size, dtype=dtype, device=device)
     return empty
 
 
@@ -322,7 +323,10 @@ class PagedKV:
              out_indices=None, stream=None):
         """The plan's tokens in 16 bits: rows ``[total_q, num_kv_heads, 128]``,
         or, with ``out_indices`` (a page of ``k`` / ``v`` for each of the
-        plan's pages), pages of the given 16-bit pools ``k`` and ``v``."""
+        plan's pages), pages of the given 16-bit pools ``k`` and ``v``.  A
+        token on a bad page (negative, or found out of range by the index
+        check) leaves its row of a given ``k`` or ``v`` as it was, and is
+        zeros in one that is made here."""
         self._check_cache(k_pool, v_pool, k_scales, v_scales, kv_indices)
         row = self.num_kv_heads * self.head_dim
         out_pages = 0
@@ -340,7 +344,9 @@ class PagedKV:
             out_pages = k.shape[0]
         else:
             ks = vs = row
-            empty = _empty(stream)
+            # both made here: the kernel writes bad pages' rows, too
+            out_pages = C.PA_KV_ZERO_BAD_ROWS if k is None and v is None else 0
+            empty = _empty(stream, torch.empty if out_pages else torch.zeros)
             if k is None:
                 k = empty(self._row_shape, dtype=self._row_dtype, device=self.device)
             else:

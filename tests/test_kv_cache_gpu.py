@@ -419,3 +419,43 @@ def test_read_allocates_for_the_given_stream():
     got = pk.read(*dev, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("check", [False, True])
+@pytest.mark.parametrize("block", [4, 16, 64])
+def test_read_makes_zeros_of_bad_pages(block, check):
+    """Rows that read makes itself hold nothing of the allocator's last user:
+    tokens on a bad page are zeros, as attention takes them."""
+    from serving_attention_paged_b200 import pagedattn as C
+    c = Cache([100, 70], [90, 70], 64, block, "bf16", "e4m3", seed=50)
+    dev = c.device()
+    bad = c.indices.copy()
+    bad[1] = c.num_pages if check else -5  # request 0, tokens 64 .. 99: rows 54 .. 89
+    bad[3] = -1                            # request 1, tokens 64 .. 69: the last 6 rows
+    pk = c.plan(flags=C.PA_FLAG_CHECK_INDICES if check else 0)
+    good = pk.read(*dev)
+    idx = torch.from_numpy(bad).cuda()
+
+    def verify(got):
+        want = torch.where(zero[:, None, None], torch.zeros((), dtype=torch.bfloat16), good[w].cpu())
+        assert torch.equal(got.cpu(), want)
+
+    zero = torch.zeros(160, dtype=torch.bool)
+    zero[54:90], zero[154:] = True, True
+    for given in (None, "k", "v"):
+        torch.cuda.synchronize()
+        dirty = [torch.full((160, c.hkv, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+                 for _ in range(2)]
+        del dirty  # the next blocks of this size
+        mine = torch.full((160, c.hkv, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+        got = pk.read(*dev[:4], idx, **({given: mine} if given else {}))
+        torch.cuda.synchronize()
+        for w, name in enumerate("kv"):
+            if name == given:
+                assert got[w] is mine and (mine[54:90] == 5).all() and (mine[154:] == 5).all()
+                assert torch.equal(mine[:54], good[w][:54])
+            else:
+                verify(got[w])
+    if check:
+        with pytest.raises(C.PagedAttnError):
+            pk.check()
