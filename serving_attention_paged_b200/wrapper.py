@@ -158,14 +158,14 @@ class PagedDecode:
         if lse is None:
             lse = empty(self.batch, self.num_qo_heads, dtype=torch.float32, device=self.device)
         if self.prefix_len:
-            C.pa_cascade_run(self.plan, q, k_pool, v_pool, prefix_indices, kv_indices, o, lse,
-                             self.workspace, self.workspace.numel(), stream)
+            _launch(self._dev, stream, C.pa_cascade_run, self.plan, q, k_pool, v_pool,
+                    prefix_indices, kv_indices, o, lse, self.workspace, self.workspace.numel())
         elif options is not None:
             _launch(self._dev, stream, C.pa_run_options, self.plan, options, q, k_pool, v_pool,
                     kv_indices, o, lse, self.workspace, self.workspace.numel())
         else:
-            C.pa_run(self.plan, q, k_pool, v_pool, kv_indices, o, lse, self.workspace,
-                     self.workspace.numel(), stream)
+            _launch(self._dev, stream, C.pa_run, self.plan, q, k_pool, v_pool, kv_indices, o, lse,
+                    self.workspace, self.workspace.numel())
         return o, lse
 
     def check(self, stream=None) -> int:
@@ -226,8 +226,8 @@ class PagedPrefill:
             _launch(self._dev, stream, C.pa_prefill_run_options, self.plan, options, q, k_pool,
                     v_pool, kv_indices, o, lse, self.workspace, self.workspace.numel())
         else:
-            C.pa_prefill_run(self.plan, q, k_pool, v_pool, kv_indices, o, lse, self.workspace,
-                             self.workspace.numel(), stream)
+            _launch(self._dev, stream, C.pa_prefill_run, self.plan, q, k_pool, v_pool, kv_indices,
+                    o, lse, self.workspace, self.workspace.numel())
         return o, lse
 
     def check(self, stream=None) -> int:
