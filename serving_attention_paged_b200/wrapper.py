@@ -61,7 +61,11 @@ def _empty(stream, make=torch.empty):
         return make
 
     def empty(*size, dtype, device):
-        on = torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream
+        on = stream
+        if isinstance(stream, int):  # handles 0 and 1 (cudaStreamLegacy): the default stream,
+            # of which ExternalStream would make another one
+            on = (torch.cuda.default_stream(device) if stream in (0, 1)
+                  else torch.cuda.ExternalStream(stream, device))
         with torch.cuda.stream(on):
             return make(*size, dtype=dtype, device=device)
     return empty

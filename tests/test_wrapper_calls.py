@@ -46,3 +46,30 @@ def test_runs_go_to_the_plans_device(name, kw, dev, stream, device, monkeypatch)
     plan.run(1, 2, 3, 4, o=6, lse=7, stream=stream, **kw)
     assert seen == [(dev, 100 + dev if stream is None else stream)]
     assert device.current == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("handle", [0, 1, "default", "side"])
+def test_outputs_come_from_the_given_handles_pool(handle):
+    """A raw handle, the legacy default stream's (0, or cudaStreamLegacy = 1)
+    included: outputs are blocks of that stream's memory, not of some other
+    stream's, on which earlier work may still use them."""
+    from serving_attention_paged_b200 import workloads as W
+    from serving_attention_paged_b200.wrapper import PagedDecode
+    w = W.make_workload("handles", [40, 17], num_qo_heads=8, num_kv_heads=2, page_size=16,
+                        dtype="f16", seed=3)
+    t = {k: v.cuda() for k, v in w.materialize().items()}
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    handle = {"default": torch.cuda.default_stream().cuda_stream,
+              "side": side.cuda_stream}.get(handle, handle)
+    pd = PagedDecode(w.kv_indptr, w.last_page_len, num_qo_heads=8, num_kv_heads=2, page_size=16,
+                     dtype="f16", sm_scale=w.sm_scale, num_pages=w.num_pages, stream=handle)
+    outputs = pd.run(t["q"], t["k_pool"], t["v_pool"], t["kv_indices"], stream=handle)
+    torch.cuda.synchronize()
+    assert pd.check(stream=handle) == -1
+    want = side.cuda_stream if handle == side.cuda_stream else 0
+    for x in (*outputs, pd.workspace):
+        owner = [s["stream"] for s in torch.cuda.memory_snapshot()
+                 if s["address"] <= x.data_ptr() < s["address"] + s["total_size"]]
+        assert owner == [want]
