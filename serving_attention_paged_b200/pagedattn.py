@@ -13,7 +13,6 @@ import ctypes
 import os
 
 import numpy as np
-import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpagedattn.so")
 if not os.path.exists(_LIB_PATH):
@@ -129,6 +128,8 @@ def _ptr(x):
 
 def _stream(s):
     if s is None:  # torch's current stream of the current device
+        import torch  # addresses and stream handles do without it
+
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return s if isinstance(s, int) else s.cuda_stream
 
