@@ -10,6 +10,7 @@
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
 pa_status from_cuda(int e) { return e == 0 ? PA_OK : PA_ERR_CUDA; }
 
@@ -44,8 +45,7 @@ pa_status check_options(const pa_plan_s& plan, const pa_attention_options& o) {
   const pa_problem& pr = plan.prob;
   if (o.logit_cap != 0.f && !(o.logit_cap >= 0x1p-20f && o.logit_cap <= 0x1p20f))
     return PA_ERR_INVALID_ARG;  // NaN too
-  const auto misaligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; };
-  if (misaligned(o.k_scales) || misaligned(o.v_scales) || misaligned(o.alibi_slopes))
+  if (!aligned4(o.k_scales) || !aligned4(o.v_scales) || !aligned4(o.alibi_slopes))
     return PA_ERR_INVALID_ARG;
   if (o.k_scales || o.v_scales || o.scale_block != 0) {
     if (plan.prefill) return PA_ERR_UNSUPPORTED;
@@ -75,7 +75,7 @@ pa_status check_kv_args(pa_plan_t plan, const void* k, int64_t k_stride, const v
   if (!rows_valid(*plan, k, k_stride) || !rows_valid(*plan, v, v_stride))
     return PA_ERR_INVALID_ARG;
   if (!k_pool || !v_pool || !aligned16(k_pool) || !aligned16(v_pool) || !k_scales || !v_scales ||
-      !kv_indices)
+      !kv_indices || !aligned4(k_scales) || !aligned4(v_scales) || !aligned4(kv_indices))
     return PA_ERR_INVALID_ARG;
   return PA_OK;
 }
@@ -184,7 +184,8 @@ pa_status pa_kv_read(pa_plan_t plan, const void* k_pool, const void* v_pool,
   if (st != PA_OK) return st;
   if (d_out_indices) {
     const int64_t row = int64_t(plan->prob.num_kv_heads) * plan->prob.head_dim;
-    if (k_stride != row || v_stride != row || num_out_pages < 0) return PA_ERR_INVALID_ARG;
+    if (k_stride != row || v_stride != row || num_out_pages < 0 || !aligned4(d_out_indices))
+      return PA_ERR_INVALID_ARG;
     // pool rows are 32-bit indices inside the kernel
     if (num_out_pages > int64_t(UINT32_MAX) / plan->prob.page_size) return PA_ERR_UNSUPPORTED;
   }
