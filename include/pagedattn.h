@@ -442,9 +442,11 @@ pa_status pa_merge_state(const void* o_a, const float* lse_a, const void* o_b,
  * memory, a host program that does not own the process's allocator, a path
  * that must not take cudaMalloc's implicit synchronisation).  The source
  * pages have no counterpart: this is a convenience of this library.
- * The workspace is a fixed 8 MiB array inside libpagedattn.so on every GPU
- * that loads it, held until the process exits; a plan needing more
- * (pa_plan_workspace_bytes > 8 MiB) is rejected with
+ * The workspace is a fixed array inside libpagedattn.so on every GPU that
+ * loads it, held until the process exits: 8 MiB, and 1 MiB for the requests'
+ * lengths (4 bytes each), which do not count; a plan needing more
+ * (pa_plan_workspace_bytes, for rotary plans as it is, for others less 4 bytes
+ * per request rounded up to 256, above 8 MiB) is rejected with
  * PA_ERR_WORKSPACE_TOO_SMALL before anything is enqueued, and cascade and
  * prefill plans with PA_ERR_INVALID_ARG.  Nothing is allocated: each call uploads the plan
  * into the array (as pa_plan_upload) and runs it (as pa_run).  The first call
