@@ -118,12 +118,13 @@ def measured_peak():
 # while their digest matches)
 _CSRC = "serving_attention_paged_b200/csrc/"
 KERNEL_SOURCES = {
-    "decode_tc": [_CSRC + f for f in ("decode_tc_kernel.cuh", "decode_tc.cu", "common.cuh",
-                                      "tcgen05.cuh", "launch.cuh")],
-    "decode": [_CSRC + f for f in ("decode.cu", "decode_kernel.cuh", "common.cuh", "launch.cuh")],
+    "decode_tc": [_CSRC + f for f in ("decode_tc_kernel.cuh", "decode_tc.cu", "score.cuh",
+                                      "common.cuh", "tcgen05.cuh", "launch.cuh")],
+    "decode": [_CSRC + f for f in ("decode.cu", "decode_kernel.cuh", "score.cuh", "common.cuh",
+                                   "launch.cuh")],
     "cascade": [_CSRC + f for f in ("cascade.cu", "attn_tile.cuh", "tcgen05.cuh")],
-    "prefill": [_CSRC + f for f in ("prefill.cu", "attn_tile.cuh", "tcgen05.cuh", "common.cuh",
-                                    "plan.cpp")],
+    "prefill": [_CSRC + f for f in ("prefill.cu", "attn_tile.cuh", "tcgen05.cuh", "score.cuh",
+                                    "common.cuh", "plan.cpp")],
 }
 
 
