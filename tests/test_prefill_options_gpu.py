@@ -92,3 +92,21 @@ def test_small_scores_under_a_cap_are_exact_to_fp32():
         off = to_np(lse)[:, 0] / exact - 1.0
         assert abs(off.mean()) <= 3 * 2.0 ** -24, dtype
         assert np.abs(off).max() <= 8 * 2.0 ** -24, dtype
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("group", [1, 4, 8])
+def test_appends_to_long_contexts(group, dtype):
+    """70 new tokens behind 16,500 and 20,011, with steep, flat and no bias."""
+    from serving_attention_paged_b200.wrapper import PagedPrefill
+    c = Case([16570, 20011], group, 64, dtype, hkv=1, seed=31 + group, qo=[70, 33])
+    w = c.w
+    c.slopes = torch.tensor([0.5, 1e-4, 0.0, 0.01] * 2)[:group].clone()
+    pf = PagedPrefill(w.qo_indptr, w.kv_indptr, w.last_page_len, num_qo_heads=group, num_kv_heads=1,
+                      page_size=64, dtype=dtype, sm_scale=w.sm_scale, num_pages=w.num_pages)
+    for cap, slopes in ((30.0, True), (3.0, False), (0.0, True)):
+        got = c.run(pf, cap, slopes)
+        ref = c.expected(qo_indptr=w.qo_indptr, logit_cap=cap,
+                         alibi_slopes=c.slopes if slopes else None)
+        assert np.isfinite(got[0]).all()
+        assert_close(*got, *ref, dtype, f"G={group} cap={cap} {slopes}")
