@@ -332,8 +332,13 @@ pa_status pa_prefill_run(pa_plan_t plan, const void* q, const void* k_pool, cons
  * their sum to 2^-18 of that largest weight, whatever the length.  Where V
  * scales differ by more than 2^20 between blocks of like weight, elements in
  * which the large blocks' codes are 0 lose the precision of the small ones.
- * Both kernels sum in fp32, in which equal weights below 2^-24 of the largest
- * can vanish beside it.
+ * Over 16-bit pools it holds p as two values of the input type (fp16: steps of
+ * 2^-31 of the largest).  Prefill holds p in fp16 (11 bits, steps no finer
+ * than 2^-28 of the largest) or as two bf16.  All sum in fp32, in which equal weights below
+ * 2^-24 of the largest can vanish beside it.  Runs without options carry
+ * nothing on: over 8-bit pools on the tensor cores weights have steps of
+ * 2^-21 of the largest, in fp16 runs of 2^-24, and a tail of smaller ones is
+ * lost (at 131,072 tokens behind a sink of 0.9, up to 0.02 of the values).
  *
  * Scores: with s = sm_scale <q, k> (and the positions' rotation, if any),
  *   s <- logit_cap * tanh(s / logit_cap)     if logit_cap > 0, then
@@ -395,6 +400,8 @@ pa_status pa_kv_plan_create(const pa_problem* problem, int32_t scale_block,
  *           is exact but for codes that become subnormal);
  *   codes of N = x / scale, rounded to nearest even, saturating (infinities
  *           too); NaN stays NaN.
+ * Ratio, product and quotient are formed in fp32, so between scales that are
+ * no powers of two (another writer's) they are rounded there first.
  * Nothing else of the pools and scales is written, rows of the block past the
  * request's last token included.  A block may receive tokens
  * through one place of the tables only (two requests appending into one block

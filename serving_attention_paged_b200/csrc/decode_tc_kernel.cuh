@@ -45,7 +45,8 @@
 // E4M3 terms, each the rounded residual of the previous ones scaled by 16:
 // q, after a per-head power-of-two scale, into 2 terms for bf16 and 3 for
 // fp16 (exact: 4 significant bits each), P into 4 terms (16 significant
-// bits).  Term k of head h is column k * G + h of S^T (resp. O^T); the
+// bits; a small weight fewer: the terms' smallest step is 2^-21 of the
+// reference's weight).  Term k of head h is column k * G + h of S^T (resp. O^T); the
 // softmax (resp. epilogue) adds the columns back with weights 16^-k.
 // Options (kExt; pa_run_options).  8-bit pools: the K and the V half of a ring
 // stage have barriers of their own (kSep).  K is free once S has been computed,
@@ -55,8 +56,8 @@
 // HBM needs 2,800.  Block scales ride ahead of their K rows: each loader lane
 // copies its tokens' K and V scale with 4-byte cp.async into one of four slots
 // with a barrier each.  (Loaded into registers a step ahead and stored, they
-// cost the ragged batch 140 us for 129, fetched by three warps of their own
-// 136 us.)  Slot t % 4 is refilled for tile t + 4 after V(t + 3), so after
+// cost the ragged batch 140 us where this took 129, fetched by three warps of
+// their own 136 us.)  Slot t % 4 is refilled for tile t + 4 after V(t + 3), so after
 // P V(t), which the softmax's reading of tile t precedes.  The K scale
 // multiplies the token's scores; the V scale v enters through the weights,
 // w = 2^(s - m) v in P's place, with the lazy reference m kept on s + log2 v,
@@ -64,11 +65,15 @@
 // 2^(s - m), and o = sum w c / sum 2^(s - m) needs no second reference
 // (|log2 v| <= 60: both sums stay far inside fp32).  The cap and the distance
 // bias are applied to the scores before the maximum (score.cuh).
-// Measured with block scales (one B200, launches replayed from a graph): 64
-// ragged requests of 353K tokens, group 4, 129 us (725 MB, 5.6 TB/s; 131 us
-// with one scale per tensor and no options); 16 x 4,096 tokens 32 us; 48
-// requests of one-token pages at group 8, a scale per token, 77 us (61 us on
-// 16-token pages: scattered scales double the requests to memory).
+// What a weight loses below the smallest step of its terms is carried to the
+// same thread's next tile (split_p).
+// Measured with block scales (one B200, launches replayed from a graph on inputs
+// that rotate past L2): 64 ragged requests of 353K tokens, group 4, 134 us (725
+// MB, 5.4 TB/s; 133 us with one scale per tensor and no options); 16 x 4,096
+// tokens 34 us; 48 requests of one-token pages at group 8, a scale per token,
+// 85 us (71 us on 16-token pages: scattered scales double the requests to
+// memory; 59 us without options).  The fourth term and the carry cost group 4
+// 1 % and group 8, whose softmax warps are the bound, 6 to 10 %.
 // Q^T, S^T, P^T and O^T are double buffered so a CTA's next piece starts while
 // the previous one finishes.  The warps meet only on mbarriers; every wait is
 // bounded, and every parity wait targets a barrier whose previous phase the

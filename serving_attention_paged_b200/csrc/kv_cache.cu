@@ -26,9 +26,11 @@
 // Both are bound by HBM; a decode step's few tokens by the launch and the
 // chain span -> page index -> row.  No atomics on results: a block's scale is
 // decided by one warp or CTA.
-// Measured (one B200, 8 kv heads): 66,934 tokens in 64-token blocks 72 us (411 MB,
-// 5.7 TB/s), 8,192 in 16-token blocks 9.7 us, 128 single tokens 3.0 us, 98,277
-// tokens read back 99 us (604 MB, 6.1 TB/s).
+// Measured (one B200, 8 kv heads; launches replayed from a graph on inputs that
+// rotate past L2): 66,934 tokens in 64-token blocks 75 us (411 MB, 5.5 TB/s), in
+// 1,024-token blocks, read twice, 102 us; 8,192 in 16-token blocks 13.7 us (50
+// MB, 3.7 TB/s; 1,024 CTAs where 592 are resident at a time); 128 single tokens
+// 4.8 us after a flush of L2; 98,277 tokens read back 103 us (604 MB, 5.9 TB/s).
 #include <cuda_runtime.h>
 
 #include "common.cuh"

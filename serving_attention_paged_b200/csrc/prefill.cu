@@ -75,7 +75,8 @@
 // rows see no key of the last tile then runs its S and softmax fully masked,
 // which keeps the two halves' tiles aligned, but no P V: 0 x V would carry
 // an infinity or NaN among the tile's values into rows that do not see it.  Measured for 8 x 1,024 appended tokens (fp16,
-// group 4, 206 GFLOP): cap and bias 306 us, cap 293, bias 251, neither 228.
+// group 4, 206 GFLOP): cap and bias 332 us, cap 320, bias 257, neither 229
+// (bf16: both 418, neither 325).
 // Every mbarrier wait is bounded; on a timeout the kernel records it in the
 // workspace status word and unwinds instead of hanging.  Every parity wait
 // targets a barrier whose previous phase the waiting thread has itself
@@ -599,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w[e] = pack2(Tag{}, p2.x, p2.y, r0, r1);
                 float q0, q1;
                 wl[e] = pack2(Tag{}, p2.x - r0, p2.y - r1, q0, q1);
-              } else {
+              } else {  // fp16: 11 bits, so o is within 2^-11 |v| of the sum over p
                 const __half2 hp = __floats2half2_rn(p2.x, p2.y);
                 w[e] = *reinterpret_cast<const uint32_t*>(&hp);
               }
