@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kn = kt + 1;  // the K tile issued this step
       if (kn < nt) {
         const int s = kn % kKStages;
-        if (kn >= kKStages) ok = mbar_wait(bar(kBarKEmpty + s), ((kn / kKStages) - 1) & 1);
+        if (kn >= kKStages) ok = mbar_wait_warp(bar(kBarKEmpty + s), ((kn / kKStages) - 1) & 1);
         if (!ok) break;
         load_tile(&tmap_k, sb + kOffK + s * kKVBytes, rnext, bar(kBarKFull + s));
         if (kn & 1) rv1 = rnext;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (kt >= 0) {
         const int s = kt % kVStages;
-        if (kt >= kVStages) ok = mbar_wait(bar(kBarVEmpty + s), ((kt / kVStages) - 1) & 1);
+        if (kt >= kVStages) ok = mbar_wait_warp(bar(kBarVEmpty + s), ((kt / kVStages) - 1) & 1);
         if (!ok) break;
         load_tile(&tmap_v, sb + kOffV + s * kKVBytes, (kt & 1) ? rv1 : rv0, bar(kBarVFull + s));
       }

@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
       auto step = [&](Pg& pv, const Pg& pk) -> bool {
         if (wv.pi >= p1) return false;
         if (t >= kStages) {  // P V(t - 3) done: its V stage and tile t - 3's scales are free
-          ok = mbar_wait(bar(L::kBarVEmpty + t % kStages), ((t / kStages) - 1) & 1);
+          ok = mbar_wait_warp(bar(L::kBarVEmpty + t % kStages), ((t / kStages) - 1) & 1);
           if (!ok) return false;
         }
         copy(wv, pv, a.v_pool, sb + L::kOffRing + (t % kStages) * kStageBytes + kVOff,
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
         if (wk.pi < p1) {
           const int n = t + 1;
           if (n >= kStages) {  // S(n - 3) done
-            ok = mbar_wait(bar(L::kBarEmpty + n % kStages), ((n / kStages) - 1) & 1);
+            ok = mbar_wait_warp(bar(L::kBarEmpty + n % kStages), ((n / kStages) - 1) & 1);
             if (!ok) return false;
           }
           load_k(n, pk);
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tc_kernel(const TcAr
     auto step = [&](Pg& pg) -> bool {
       if (pi >= p1) return false;
       const int s = t % kStages;
-      if (t >= kStages && !mbar_wait(bar(L::kBarEmpty + s), ((t / kStages) - 1) & 1)) {
+      if (t >= kStages && !mbar_wait_warp(bar(L::kBarEmpty + s), ((t / kStages) - 1) & 1)) {
         ok = false;
         return false;
       }

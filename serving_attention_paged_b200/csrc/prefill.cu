@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kn = kt + 1;
         if (kn < it.ntiles) {
           const int g = kg + kn, s = g % kKStages;
-          if (g >= kKStages) ok = mbar_wait(bar(kBarKEmpty + s), ((g / kKStages) - 1) & 1);
+          if (g >= kKStages) ok = mbar_wait_warp(bar(kBarKEmpty + s), ((g / kKStages) - 1) & 1);
           if (!ok) break;
           load_tile(&tmap_k, sb + kOffK + s * kKVBytes, rnext, bar(kBarKFull + s));
           if (kn & 1) rv1 = rnext;
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         } else {
           const int g = vg + kt, s = g % kVStages;
-          if (g >= kVStages) ok = mbar_wait(bar(kBarVEmpty + s), ((g / kVStages) - 1) & 1);
+          if (g >= kVStages) ok = mbar_wait_warp(bar(kBarVEmpty + s), ((g / kVStages) - 1) & 1);
           if (!ok) break;
           load_tile(&tmap_v, sb + kOffV + s * kKVBytes, (kt & 1) ? rv1 : rv0, bar(kBarVFull + s));
         }
