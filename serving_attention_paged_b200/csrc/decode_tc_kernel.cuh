@@ -68,12 +68,13 @@
 // What a weight loses below the smallest step of its terms is carried to the
 // same thread's next tile (split_p).
 // Measured with block scales (one B200, launches replayed from a graph on inputs
-// that rotate past L2): 64 ragged requests of 353K tokens, group 4, 134 us (725
-// MB, 5.4 TB/s; 133 us with one scale per tensor and no options); 16 x 4,096
+// that rotate past L2): 64 ragged requests of 353K tokens, group 4, 133 us (725
+// MB, 5.4 TB/s; 135 us with one scale per tensor and no options); 16 x 4,096
 // tokens 34 us; 48 requests of one-token pages at group 8, a scale per token,
-// 85 us (71 us on 16-token pages: scattered scales double the requests to
-// memory; 59 us without options).  The fourth term and the carry cost group 4
-// 1 % and group 8, whose softmax warps are the bound, 6 to 10 %.
+// 83 us (67 us on 16-token pages, the rest being the scattered scales'
+// requests; 59 us on one-token pages without options).  The fourth term and the
+// carry cost group 4 1 % and group 8, whose softmax warps are the bound, 6 to
+// 10 %.
 // Q^T, S^T, P^T and O^T are double buffered so a CTA's next piece starts while
 // the previous one finishes.  The warps meet only on mbarriers; every wait is
 // bounded, and every parity wait targets a barrier whose previous phase the

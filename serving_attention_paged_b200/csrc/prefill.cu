@@ -75,8 +75,8 @@
 // rows see no key of the last tile then runs its S and softmax fully masked,
 // which keeps the two halves' tiles aligned, but no P V: 0 x V would carry
 // an infinity or NaN among the tile's values into rows that do not see it.  Measured for 8 x 1,024 appended tokens (fp16,
-// group 4, 206 GFLOP): cap and bias 332 us, cap 320, bias 257, neither 229
-// (bf16: both 418, neither 325).
+// group 4, 206 GFLOP; inputs that rotate past L2): cap and bias 326 us, cap
+// 316, bias 256, neither 227 (bf16: both 415, neither 309).
 // Every mbarrier wait is bounded; on a timeout the kernel records it in the
 // workspace status word and unwinds instead of hanging.  Every parity wait
 // targets a barrier whose previous phase the waiting thread has itself

@@ -65,7 +65,7 @@ inline void set_score_args(const pa_attention_options& o, ScoreArgs* a, float* s
 // 1.3e-8, below fp32's rounding.  (Degree 3 is one operation less and 5.4e-7
 // off, all one way for small scores: 9e-4 of a score of 1,600; on |y| <= 5/16
 // it is right, but scores beyond take the longer polynomial: 376 us a prefill
-// for 332.)  |x| <= mid: |score_scale * x| <= 1.
+// where degree 4 took 332.)  |x| <= mid: |score_scale * x| <= 1.
 struct CapPoly {
   float k[5], small, mid;
 };
